@@ -1,7 +1,9 @@
 /*
  * dwconv.h - C ABI of a B200 (sm_100a) library for the depthwise-convolution hot path of a
  * conformer speech encoder: the time-axis depthwise conv1d (forward, data gradient, weight
- * and bias gradients) and the fused depthwise-striding subsampler front.
+ * and bias gradients) and the fused depthwise-striding subsampler front; and for the row
+ * operations on both sides of the conv in every module: layer norm, dropout with the residual
+ * add, and the two in one pass, forward and backward.
  *
  * Conventions shared by every entry point
  *  - Memory: every tensor pointer is a DEVICE pointer owned by the caller.  The library
@@ -410,6 +412,130 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
                             int KT, int KF, int stride_t, int stride_f, int pad_t, int pad_b,
                             int pad_f, dw_dtype_t io_dtype, void *workspace,
                             size_t workspace_bytes, dw_stream_t stream);
+
+/*
+ * The residual path: layer norm over the channels of a frame, dropout with the residual add, and
+ * the two in one pass (a module's exit and the next module's entry).  Common to the six entry
+ * points below:
+ *
+ *  - x, y and the like are [B][T][C] io_dtype, channels last; gamma, beta, mean, rstd and the
+ *    gradients of gamma and beta are float32, and so is the arithmetic.  Every output is
+ *    written in full: frames t >= len_b as +0.0 (mean and rstd too).  Invalid frames of the
+ *    inputs are never read.  No output may overlap an input or another output.
+ *  - A packed batch [N][C] is B = 1, T = N with `lengths` pointing at its last offset
+ *    (offsets + B): rows no sequence covers are then written as zeros.  A streaming step of B
+ *    streams with one frame each is T = 1.
+ *  - Any C from 1 to 4,194,304 and any alignment.  Activations on 16-byte boundaries take the
+ *    vector kernels for every C up to 8192 channels (4096 of float32), whether or not the rows
+ *    after the first start on 16 bytes; other calls take a narrower (slower) kernel.
+ *  - Dropout: rng points at two device uint64, {seed, offset}, read when the kernel runs, so a
+ *    captured graph draws new numbers once the program changes them on the device.  Element e
+ *    of the tensor (its flat index, from 0) uses the 16 bits number e mod 8 (word (e mod 8)/2,
+ *    low half first) of the Philox4x32-10 block with key = seed and counter = e/8 + 2^64 offset
+ *    (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011).  It is
+ *    dropped when they are below thr = floor(65536 p + 1/2): p is rounded to a multiple of 2^-16.
+ *    A dropped element counts as zero whatever it holds; a kept one is multiplied by
+ *    m = alpha 65536 / (65536 - thr) (0 when thr = 65536), so the rounding of p leaves the mean
+ *    of the sum as it is.  No mask is stored: the backward pass draws it again from the same rng
+ *    values, p and sizes.  alpha is the residual branch's factor (1, or 1/2 for a half-step
+ *    module).  0 <= p <= 1; with thr = 0 nothing is drawn and rng may be NULL.
+ */
+
+/*
+ * dw_layernorm_fwd - layer norm over C of every valid frame:
+ *
+ *   mean = sum_c x / C,  rstd = 1 / sqrt(sum_c (x - mean)^2 / C + eps)
+ *   y[b,t,c] = [t < len_b] ((x[b,t,c] - mean) * rstd * gamma[c] + beta[c])
+ *
+ * float32 sums, the variance from centred values; one rounding to io_dtype.
+ *
+ *  gamma, beta  [C] float32, device; either may be NULL (ones, zeros)
+ *  mean, rstd   [B][T] float32, device, for the backward pass; either may be NULL
+ *  eps          finite, >= 0
+ */
+dw_status_t dw_layernorm_fwd(const void *x, const float *gamma, const float *beta, void *y, float *mean,
+                             float *rstd, const int32_t *lengths, int64_t B, int64_t T, int64_t C, float eps,
+                             dw_dtype_t io_dtype, dw_stream_t stream);
+
+/*
+ * dw_layernorm_bwd_workspace_size - bytes of device workspace dw_layernorm_bwd and
+ * dw_dropout_add_layernorm_bwd need for these sizes (independent of pointers, dtype and device);
+ * 0 for invalid sizes and when B*T == 0.
+ */
+size_t dw_layernorm_bwd_workspace_size(int64_t B, int64_t T, int64_t C);
+
+/*
+ * dw_layernorm_bwd - gradients of dw_layernorm_fwd, with xh = (x - mean) * rstd, g = dy * gamma:
+ *
+ *   dx = [t < len_b] rstd (g - sum_c g / C - xh sum_c (g xh) / C)
+ *   dgamma[c] = sum_{valid b,t} dy xh,   dbeta[c] = sum_{valid b,t} dy
+ *
+ * dgamma and dbeta: float32 partial sums per block go to `workspace` and a second kernel adds
+ * them in a fixed order: bitwise reproducible for given sizes on a given GPU model.  No atomics.
+ *
+ *  x, dy          the forward pass's input and the gradient of y;  dx the gradient of x
+ *  mean, rstd     [B][T] float32 from the forward pass
+ *  gamma          as in the forward pass (NULL: ones)
+ *  dgamma, dbeta  [C] float32, device, overwritten; either or both may be NULL (not wanted)
+ *  workspace      at least dw_layernorm_bwd_workspace_size(B, T, C) bytes, 16-byte aligned,
+ *                 contents on entry ignored; may be NULL when dgamma and dbeta are.
+ *  With B*T == 0 the gradients are written as zeros.
+ */
+dw_status_t dw_layernorm_bwd(const void *x, const void *dy, const float *gamma, const float *mean,
+                             const float *rstd, void *dx, float *dgamma, float *dbeta, const int32_t *lengths,
+                             int64_t B, int64_t T, int64_t C, dw_dtype_t io_dtype, void *workspace,
+                             size_t workspace_bytes, dw_stream_t stream);
+
+/*
+ * dw_dropout_add_fwd - y[b,t,c] = [t < len_b] (residual[b,t,c] + [kept] m x[b,t,c]); residual may
+ * be NULL (zeros).  The sum is rounded to io_dtype once.
+ */
+dw_status_t dw_dropout_add_fwd(const void *x, const void *residual, void *y, const uint64_t *rng, double p,
+                               double alpha, const int32_t *lengths, int64_t B, int64_t T, int64_t C,
+                               dw_dtype_t io_dtype, dw_stream_t stream);
+
+/*
+ * dw_dropout_add_bwd - dx[b,t,c] = [t < len_b] [kept] m dy[b,t,c], with the forward pass's rng, p
+ * and alpha.  (The residual's gradient is dy itself on the valid frames.)
+ */
+dw_status_t dw_dropout_add_bwd(const void *dy, void *dx, const uint64_t *rng, double p, double alpha,
+                               const int32_t *lengths, int64_t B, int64_t T, int64_t C, dw_dtype_t io_dtype,
+                               dw_stream_t stream);
+
+/*
+ * dw_dropout_add_layernorm_fwd - dropout, the residual add and the layer norm of the sum:
+ *
+ *   s = residual + [kept] m x,   h = s rounded to io_dtype,   y = layer norm of s over C
+ *
+ * The norm takes the float32 sum, not its rounding, so y carries one rounding like h.
+ *
+ *  residual     may be NULL (zeros)
+ *  h            the new residual stream; may be NULL (not wanted)
+ *  y, mean, rstd, gamma, beta, eps: as dw_layernorm_fwd
+ */
+dw_status_t dw_dropout_add_layernorm_fwd(const void *x, const void *residual, const uint64_t *rng, double p,
+                                         double alpha, const float *gamma, const float *beta, void *h, void *y,
+                                         float *mean, float *rstd, const int32_t *lengths, int64_t B, int64_t T,
+                                         int64_t C, float eps, dw_dtype_t io_dtype, dw_stream_t stream);
+
+/*
+ * dw_dropout_add_layernorm_bwd - gradients of dw_dropout_add_layernorm_fwd: with dl the dx of
+ * dw_layernorm_bwd (x = h, the stored sum),
+ *
+ *   ds = [t < len_b] (dh + dl),   dresidual = ds,   dx = [kept] m ds
+ *
+ * each rounded once from the float32 ds.
+ *
+ *  dy, dh      the gradients of y and of h (dh NULL: zeros)
+ *  dresidual   may be NULL (not wanted)
+ *  dgamma, dbeta, workspace: as dw_layernorm_bwd
+ */
+dw_status_t dw_dropout_add_layernorm_bwd(const void *dy, const void *dh, const void *h, const float *gamma,
+                                         const float *mean, const float *rstd, const uint64_t *rng, double p,
+                                         double alpha, void *dx, void *dresidual, float *dgamma, float *dbeta,
+                                         const int32_t *lengths, int64_t B, int64_t T, int64_t C,
+                                         dw_dtype_t io_dtype, void *workspace, size_t workspace_bytes,
+                                         dw_stream_t stream);
 
 /* dw_status_string - a static, human-readable name for a status code. */
 const char *dw_status_string(dw_status_t status);

@@ -1,4 +1,5 @@
-"""B200 (sm_100a) depthwise-convolution hot path of a conformer speech encoder.
+"""B200 (sm_100a) depthwise-convolution hot path of a conformer speech encoder, with the row
+operations on both sides of the conv (layer norm, dropout with the residual add).
 
 A thin binding over the C ABI of ``libdwconv_b200.so`` (declared in ``include/dwconv.h``):
 each function below has the name of the C entry point it calls and only marshals arguments
@@ -8,7 +9,8 @@ every call raises: build it with ``python -m speech_encoder_depthwise_b200.build
 
 Tensors are torch CUDA tensors, contiguous, channels last:
 x, y, dy, dx ``[B, T, C]`` (bfloat16, float16 or float32); w ``[K, C]`` float32; bias ``[C]`` float32;
-lengths ``[B]`` int32 (or None); mel ``[B, T, F]`` float32; w0, w1 ``[3, 3, C]`` float32.
+lengths ``[B]`` int32 (or None); mel ``[B, T, F]`` float32; w0, w1 ``[3, 3, C]`` float32; gamma, beta
+``[C]`` float32; mean, rstd ``[B, T]`` float32; rng ``[2]`` int64 (seed, offset).
 """
 from __future__ import annotations
 
@@ -24,6 +26,8 @@ __all__ = [
     "dwconv1d_bwd_dx_packed", "dwconv1d_bwd_dw_packed_workspace_size", "dwconv1d_bwd_dw_packed",
     "dw_subsample_fwd", "dw_subsample_fwd_simt", "dw_subsample_bwd_workspace_size", "dw_subsample_bwd", "dw_status_string", "dw_device_error", "subsample_out_shape",
     "dwconv2d_fwd", "dwconv2d_bwd_dx", "dwconv2d_bwd_dw_workspace_size", "dwconv2d_bwd_dw", "conv2d_out_shape",
+    "dw_layernorm_fwd", "dw_layernorm_bwd_workspace_size", "dw_layernorm_bwd", "dw_dropout_add_fwd",
+    "dw_dropout_add_bwd", "dw_dropout_add_layernorm_fwd", "dw_dropout_add_layernorm_bwd",
     "dw_selftest_wait_timeout",
 ]
 
@@ -38,6 +42,9 @@ _lib = None
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
+_f64 = ctypes.c_double
+_size = ctypes.c_size_t
 
 # name -> (restype, argtypes), mirroring include/dwconv.h
 SIGNATURES = {
@@ -70,6 +77,13 @@ SIGNATURES = {
                                                          _int]),
     "dwconv2d_bwd_dw": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int, _int, _int, _int, _int,
                                _int, _int, _vp, ctypes.c_size_t, _vp]),
+    "dw_layernorm_fwd": (_int, [_vp] * 7 + [_i64] * 3 + [_f32, _int, _vp]),
+    "dw_layernorm_bwd_workspace_size": (_size, [_i64] * 3),
+    "dw_layernorm_bwd": (_int, [_vp] * 9 + [_i64] * 3 + [_int, _vp, _size, _vp]),
+    "dw_dropout_add_fwd": (_int, [_vp] * 4 + [_f64] * 2 + [_vp] + [_i64] * 3 + [_int, _vp]),
+    "dw_dropout_add_bwd": (_int, [_vp] * 3 + [_f64] * 2 + [_vp] + [_i64] * 3 + [_int, _vp]),
+    "dw_dropout_add_layernorm_fwd": (_int, [_vp] * 3 + [_f64] * 2 + [_vp] * 7 + [_i64] * 3 + [_f32, _int, _vp]),
+    "dw_dropout_add_layernorm_bwd": (_int, [_vp] * 7 + [_f64] * 2 + [_vp] * 5 + [_i64] * 3 + [_int, _vp, _size, _vp]),
     "dw_status_string": (ctypes.c_char_p, [_int]),
     "dw_last_cuda_error": (_int, []),
     "dw_device_error": (_int, []),
@@ -392,6 +406,126 @@ def dwconv2d_bwd_dw(x, dy, dw, dbias, lengths, stride, pads, workspace, stream=N
                                workspace.numel() * workspace.element_size() if workspace is not None else 0,
                                _stream(stream))
     _check("dwconv2d_bwd_dw", st)
+
+
+class _Operands:
+    """Checks the tensors of one call and gives their pointers.  All of them live on the first
+    one's device; ``call`` runs there, on ``stream`` or that device's current stream."""
+
+    __slots__ = ("dev", "dtype", "shape", "B", "C", "code", "f32")
+
+    def __init__(self, x, name):
+        import torch
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.dim() != 3:
+            raise ValueError(f"{name} must have shape [B, T, C], got {tuple(x.shape)}")
+        self.dev, self.dtype, self.shape = x.get_device(), x.dtype, x.shape
+        self.B, _, self.C = self.shape
+        self.code, self.f32 = _dtype_code(x), torch.float32
+
+    def ptr(self, t, name, dtype, shape):
+        if t is None:
+            return None
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name} must be on cuda:{self.dev}, is on {t.device}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def act(self, t, name):
+        return self.ptr(t, name, self.dtype, self.shape)
+
+    def row(self, t, name):
+        return self.ptr(t, name, self.f32, self.shape[:2])
+
+    def chan(self, t, name):
+        return self.ptr(t, name, self.f32, self.shape[2:])
+
+    def lengths(self, t):
+        import torch
+        return self.ptr(t, "lengths", torch.int32, self.shape[:1])
+
+    def rng(self, t):
+        import torch
+        return self.ptr(t, "rng", torch.int64, (2,))
+
+    def workspace(self, t):
+        if t is None:
+            return None, 0
+        return self.ptr(t, "workspace", t.dtype, t.shape), t.numel() * t.element_size()
+
+    def call(self, fn, stream, *args):
+        import torch
+        handle = getattr(lib(), fn)
+        if self.dev == torch.cuda.current_device():
+            st = handle(*args, _stream(stream))
+        else:
+            with torch.cuda.device(self.dev):
+                st = handle(*args, _stream(stream))
+        if st != DW_OK:
+            raise DwError(fn, st)
+
+
+def dw_layernorm_fwd(x, gamma, beta, y, mean, rstd, lengths, eps=1e-5, stream=None):
+    """y = layer norm of x over C on the valid frames (zeros elsewhere); gamma, beta, mean and rstd
+    may be None."""
+    o = _Operands(x, "x")
+    o.call("dw_layernorm_fwd", stream, o.act(x, "x"), o.chan(gamma, "gamma"), o.chan(beta, "beta"), o.act(y, "y"),
+           o.row(mean, "mean"), o.row(rstd, "rstd"), o.lengths(lengths), *o.shape, eps, o.code)
+
+
+def dw_layernorm_bwd_workspace_size(B, T, C) -> int:
+    """Bytes of workspace ``dw_layernorm_bwd`` and ``dw_dropout_add_layernorm_bwd`` need."""
+    return int(lib().dw_layernorm_bwd_workspace_size(B, T, C))
+
+
+def dw_layernorm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, lengths, workspace, stream=None):
+    """Gradients of ``dw_layernorm_fwd`` into dx and (float32 [C], either may be None) dgamma, dbeta."""
+    o = _Operands(x, "x")
+    o.call("dw_layernorm_bwd", stream, o.act(x, "x"), o.act(dy, "dy"), o.chan(gamma, "gamma"), o.row(mean, "mean"),
+           o.row(rstd, "rstd"), o.act(dx, "dx"), o.chan(dgamma, "dgamma"), o.chan(dbeta, "dbeta"), o.lengths(lengths),
+           *o.shape, o.code, *o.workspace(workspace))
+
+
+def dw_dropout_add_fwd(x, residual, y, rng, p, alpha, lengths, stream=None):
+    """y = residual + alpha/(1-p) x on the kept elements of the valid frames, residual alone on the
+    dropped ones (residual may be None); ``rng`` is a CUDA int64 tensor {seed, offset}."""
+    o = _Operands(x, "x")
+    o.call("dw_dropout_add_fwd", stream, o.act(x, "x"), o.act(residual, "residual"), o.act(y, "y"), o.rng(rng), p,
+           alpha, o.lengths(lengths), *o.shape, o.code)
+
+
+def dw_dropout_add_bwd(dy, dx, rng, p, alpha, lengths, stream=None):
+    """Gradient of ``dw_dropout_add_fwd`` with respect to x (same rng, p and alpha) into dx."""
+    o = _Operands(dy, "dy")
+    o.call("dw_dropout_add_bwd", stream, o.act(dy, "dy"), o.act(dx, "dx"), o.rng(rng), p, alpha, o.lengths(lengths),
+           *o.shape, o.code)
+
+
+def dw_dropout_add_layernorm_fwd(x, residual, rng, p, alpha, gamma, beta, h, y, mean, rstd, lengths, eps=1e-5,
+                                 stream=None):
+    """h = ``dw_dropout_add_fwd``'s sum and y = its layer norm in one pass (residual, h, mean, rstd,
+    gamma and beta may be None)."""
+    o = _Operands(x, "x")
+    o.call("dw_dropout_add_layernorm_fwd", stream, o.act(x, "x"), o.act(residual, "residual"), o.rng(rng), p, alpha,
+           o.chan(gamma, "gamma"), o.chan(beta, "beta"), o.act(h, "h"), o.act(y, "y"), o.row(mean, "mean"),
+           o.row(rstd, "rstd"), o.lengths(lengths), *o.shape, eps, o.code)
+
+
+def dw_dropout_add_layernorm_bwd(dy, dh, h, gamma, mean, rstd, rng, p, alpha, dx, dresidual, dgamma, dbeta, lengths,
+                                 workspace, stream=None):
+    """Gradients of ``dw_dropout_add_layernorm_fwd`` from dy and dh (None: zeros) into dx, dresidual
+    and (float32 [C]) dgamma, dbeta; dresidual, dgamma and dbeta may be None."""
+    o = _Operands(dy, "dy")
+    o.call("dw_dropout_add_layernorm_bwd", stream, o.act(dy, "dy"), o.act(dh, "dh"), o.act(h, "h"),
+           o.chan(gamma, "gamma"), o.row(mean, "mean"), o.row(rstd, "rstd"), o.rng(rng), p, alpha, o.act(dx, "dx"),
+           o.act(dresidual, "dresidual"), o.chan(dgamma, "dgamma"), o.chan(dbeta, "dbeta"), o.lengths(lengths),
+           *o.shape, o.code, *o.workspace(workspace))
 
 
 def dw_selftest_wait_timeout(done, stream=None):

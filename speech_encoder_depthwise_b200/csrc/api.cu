@@ -28,24 +28,12 @@ namespace {
 
 using dwapi::cuda_status;
 
-size_t dtype_size(dw_dtype_t t) { return t == DW_F32 ? 4 : 2; }
-
-bool valid_dtype(dw_dtype_t t) { return t == DW_F32 || t == DW_BF16 || t == DW_F16; }
-
-// n = a*b*c without overflow of int64 (all >= 0)
-bool mul3(int64_t a, int64_t b, int64_t c, int64_t *n) {
-    __int128 p = static_cast<__int128>(a) * b * c;
-    if (p > static_cast<__int128>(INT64_MAX / 4)) return false;
-    *n = static_cast<int64_t>(p);
-    return true;
-}
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return pa < pb + nb && pb < pa + na;
-}
-
-bool aligned(const void *p, size_t n) { return p == nullptr || reinterpret_cast<uintptr_t>(p) % n == 0; }
+using dwapi::aligned;
+using dwapi::dtype_size;
+using dwapi::kMaxChannels;
+using dwapi::mul3;
+using dwapi::overlaps;
+using dwapi::valid_dtype;
 
 // Widest channel vector (4, 2 or 1 channels) that C and every pointer allow: activations
 // aligned to the vector, float32 parameters to 8 bytes (they are read as float2).
@@ -61,9 +49,6 @@ int pick_vec_width(int64_t C, size_t esize, std::initializer_list<const void *> 
     }
     return 1;
 }
-
-// Channel counts beyond this are rejected: frame offsets are kept in 32 bits inside a run.
-constexpr int64_t kMaxChannels = 1 << 22;
 
 dw_status_t check_conv1d_common(const void *in, const float *w, const void *out, int64_t B, int64_t T,
                                 int64_t C, int K, int pad_left, dw_dtype_t dt, int64_t *n) {

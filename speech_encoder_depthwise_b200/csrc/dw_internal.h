@@ -186,4 +186,32 @@ bool subsample_tc_eligible(const SubsampleArgs &a);
 cudaError_t subsample_tc_launch(const SubsampleArgs &a, cudaStream_t s);
 unsigned int subsample_tc_take_error();
 
+// Layer norm, dropout with the residual add, and the two in one pass, over rows of C channels.
+// Forward: s = res + [kept] mult x, h = s rounded, y = layer norm of s (plain layer norm: no res,
+// thr 0, mult 1, no h).  Backward: x is the stored sum h; dx, dres from dy and dh.
+struct ResidualArgs {
+    const void *x = nullptr, *res = nullptr;
+    const void *dy = nullptr, *dh = nullptr;
+    void *y = nullptr, *h = nullptr, *dx = nullptr, *dres = nullptr;
+    const float *gamma = nullptr, *beta = nullptr;
+    float *mean = nullptr, *rstd = nullptr;     // written forward, read backward
+    float *dgamma = nullptr, *dbeta = nullptr;
+    float *partials = nullptr;                  // workspace: [G][2][ceil4(C)] float32
+    int G = 0;                                  // partial rows
+    const int32_t *lengths = nullptr;
+    const unsigned long long *rng = nullptr;    // {seed, offset}, device
+    uint32_t thr = 0;                           // an element is dropped when its 16 bits are below it
+    float mult = 1.f;                           // factor of a kept element
+    float eps = 0.f;
+    int64_t B = 0, T = 0, C = 0;
+    int dtype = 0;                              // 0 float32, 1 bf16, 2 fp16
+    int vec16 = 0;                              // every activation on a 16-byte boundary
+};
+cudaError_t dropout_add_launch(const ResidualArgs &a, cudaStream_t s);
+cudaError_t layernorm_fwd_launch(const ResidualArgs &a, cudaStream_t s);
+// dgamma/dbeta: the number of partial rows and the workspace bytes follow from the sizes alone.
+int layernorm_bwd_partial_rows(int64_t B, int64_t T, int64_t C);
+size_t layernorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C);
+cudaError_t layernorm_bwd_launch(const ResidualArgs &a, cudaStream_t s);
+
 }  // namespace dwk
