@@ -30,6 +30,13 @@ bool disjoint(std::initializer_list<Region> outs, std::initializer_list<Region> 
     return true;
 }
 
+// Whether every activation lies on a boundary of 8 elements.
+bool oct_aligned(dw_dtype_t dt, std::initializer_list<const void *> acts) {
+    for (const void *p : acts)
+        if (!aligned(p, 8 * dtype_size(dt))) return false;
+    return true;
+}
+
 dw_status_t check_sizes(int64_t B, int64_t T, int64_t C, dw_dtype_t dt, int64_t *n) {
     if (!dwapi::valid_dtype(dt) || B < 0 || T < 0 || C < 1) return DW_ERR_INVALID_ARG;
     if (C > dwapi::kMaxChannels) return DW_ERR_UNSUPPORTED;
@@ -64,7 +71,7 @@ dw_status_t norm_fwd(dwk::ResidualArgs *a, int64_t n, float eps, dw_dtype_t dt, 
                    {a->lengths, static_cast<size_t>(a->B) * sizeof(int32_t)}}))
         return DW_ERR_INVALID_ARG;
     a->eps = eps;
-    a->vec16 = aligned(a->x, 16) && aligned(a->res, 16) && aligned(a->y, 16) && aligned(a->h, 16);
+    a->vec_oct = oct_aligned(dt, {a->x, a->res, a->y, a->h});
     return cuda_status(dwk::layernorm_fwd_launch(*a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -83,8 +90,7 @@ dw_status_t norm_bwd(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, void *works
             a->partials = static_cast<float *>(workspace);
         }
         a->G = dwk::layernorm_bwd_partial_rows(a->B, a->T, a->C);
-        a->vec16 = aligned(a->x, 16) && aligned(a->dy, 16) && aligned(a->dh, 16) && aligned(a->dx, 16) &&
-                   aligned(a->dres, 16);
+        a->vec_oct = oct_aligned(dt, {a->x, a->dy, a->dh, a->dx, a->dres});
     }
     if (n == 0 && !params) return DW_OK;
     // with no rows only dgamma and dbeta are touched
@@ -104,7 +110,7 @@ dw_status_t dropout_add(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, dw_strea
     if (!disjoint({{a->y, act}}, {{a->x, act}, {a->res, act}, {a->rng, a->thr ? 16u : 0u},
                                   {a->lengths, static_cast<size_t>(a->B) * sizeof(int32_t)}}))
         return DW_ERR_INVALID_ARG;
-    a->vec16 = aligned(a->x, 16) && aligned(a->res, 16) && aligned(a->y, 16);
+    a->vec_oct = oct_aligned(dt, {a->x, a->res, a->y});
     return cuda_status(dwk::dropout_add_launch(*a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -42,9 +42,115 @@ dropout_add_general_kernel(const T *__restrict__ x, const T *__restrict__ res, T
     }
 }
 
+// Octet-aligned tensors: a block takes a chunk of 256 U octets, all of a thread's loads first.  Most
+// chunks lie wholly within the valid or the masked frames of one item, which one division per
+// block tells; in the others every octet is looked at by itself, and those with an item's end or
+// its last valid frame inside (or past the tensor's end) go element by element.
+constexpr int kChunkOctets = 4;
+template <typename T, bool DROP, bool RES>
+__global__ void __launch_bounds__(256)
+dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *__restrict__ y,
+                         const int32_t *__restrict__ lengths, const unsigned long long *__restrict__ rng, uint32_t thr,
+                         float mult, int64_t B, int64_t Tn, int64_t C) {
+    constexpr int U = kChunkOctets, kStep = 256 * 8, kChunk = U * kStep;
+    enum { kValid, kMasked, kMixed, kNone };
+    launch_dependents();
+    const int64_t TC = Tn * C, N = B * TC, first = static_cast<int64_t>(blockIdx.x) * kChunk;
+    const bool narrow = N < (int64_t(1) << 32);
+    const auto item_of = [&](int64_t e) -> int64_t {
+        return narrow ? static_cast<uint32_t>(e) / static_cast<uint32_t>(TC) : e / TC;
+    };
+    const int64_t b = lengths ? item_of(first) : 0;
+    grid_dependency_wait();
+    Dropper D;
+    if constexpr (DROP) D.start(rng, thr);
+    const int64_t mine = first + threadIdx.x * 8;
+    int st[U];
+    {
+        const int64_t start = b * TC, lim = lengths ? start + clamp_len(lengths, b, Tn) * C : N;
+        const bool whole = first + kChunk <= N;
+        if (whole && first + kChunk <= lim) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) st[u] = kValid;
+        } else if (whole && first >= lim && first + kChunk <= start + TC) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) st[u] = kMasked;
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t e = mine + u * kStep;
+                st[u] = kNone;
+                if (e >= N) continue;
+                const int64_t item = lengths ? item_of(e) : 0, i0 = lengths ? item * TC : 0;
+                const int64_t i1 = lengths ? i0 + clamp_len(lengths, item, Tn) * C : N, i2 = lengths ? i0 + TC : N;
+                st[u] = e + 8 <= i1 ? kValid : (e >= i1 && e + 8 <= i2 ? kMasked : kMixed);
+            }
+        }
+    }
+    Oct<T> xo[U], ro[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (st[u] != kValid) continue;
+        xo[u].load(x + mine + u * kStep);
+        if constexpr (RES) ro[u].load(res + mine + u * kStep);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float f[8] = {}, q[8] = {};
+        if (st[u] == kValid) {
+            xo[u].get(f);
+            if constexpr (RES) ro[u].get(q);
+            if constexpr (DROP) D.apply(static_cast<uint64_t>(mine + u * kStep) >> 3, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = RES ? fmaf(mult, f[i], q[i]) : mult * f[i];
+        }
+        if (st[u] <= kMasked) Oct<T>::store(y + mine + u * kStep, f);
+    }
+    unsigned mixed = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mixed |= st[u] == kMixed ? 1u << u : 0u;
+#pragma unroll 1
+    for (int u = 0; mixed; ++u, mixed >>= 1) {
+        if (!(mixed & 1u)) continue;
+        const int64_t e0 = mine + u * kStep;
+        float keep[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+        if constexpr (DROP) D.apply(static_cast<uint64_t>(e0) >> 3, keep);
+        int64_t item = lengths ? item_of(e0) : 0, next = lengths ? (item + 1) * TC : N;
+        int64_t lim = lengths ? item * TC + clamp_len(lengths, item, Tn) * C : N;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t e = e0 + i;
+            if (e >= N) break;
+            if (lengths && e >= next) {
+                lim = next + clamp_len(lengths, ++item, Tn) * C;
+                next += TC;
+            }
+            float v = 0.f;
+            if (e < lim) {
+                if constexpr (RES) v = load1(res + e);
+                if (keep[i] != 0.f) v = fmaf(mult, load1(x + e), v);
+            }
+            store1(y + e, v);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_octets(const ResidualArgs &a, cudaStream_t s) {
+    const int64_t chunk = 256 * kChunkOctets * 8, blocks = (a.B * a.T * a.C + chunk - 1) / chunk;
+    const auto go = [&](auto kern) {
+        return launch_programmatic(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+                                   static_cast<const T *>(a.x), static_cast<const T *>(a.res), static_cast<T *>(a.y),
+                                   a.lengths, a.rng, a.thr, a.mult, a.B, a.T, a.C);
+    };
+    if (a.thr) return a.res ? go(dropout_add_octet_kernel<T, true, true>) : go(dropout_add_octet_kernel<T, true, false>);
+    return a.res ? go(dropout_add_octet_kernel<T, false, true>) : go(dropout_add_octet_kernel<T, false, false>);
+}
+
 }  // namespace
 
 cudaError_t dropout_add_launch(const ResidualArgs &a, cudaStream_t s) {
+    if (a.vec_oct) return with_dtype(a.dtype, [&](auto t) { return launch_octets<decltype(t)>(a, s); });
     const int64_t groups = (a.B * a.T * a.C + 7) / 8;
     const int64_t blocks = (groups + 255) / 256, most = static_cast<int64_t>(sm_count()) * 8;
     const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));

@@ -205,13 +205,21 @@ struct ResidualArgs {
     float eps = 0.f;
     int64_t B = 0, T = 0, C = 0;
     int dtype = 0;                              // 0 float32, 1 bf16, 2 fp16
-    int vec16 = 0;                              // every activation on a 16-byte boundary
+    int vec_oct = 0;                            // every activation on an 8-element boundary (16 or 32 bytes)
 };
 cudaError_t dropout_add_launch(const ResidualArgs &a, cudaStream_t s);
 cudaError_t layernorm_fwd_launch(const ResidualArgs &a, cudaStream_t s);
+// The kernels that hold a row in registers; cudaErrorNotSupported where they do not serve.
+cudaError_t layernorm_fwd_rows_bf16(const ResidualArgs &a, cudaStream_t s);
+cudaError_t layernorm_fwd_rows_f16(const ResidualArgs &a, cudaStream_t s);
+cudaError_t layernorm_fwd_rows_f32(const ResidualArgs &a, cudaStream_t s);
 // dgamma/dbeta: the number of partial rows and the workspace bytes follow from the sizes alone.
 int layernorm_bwd_partial_rows(int64_t B, int64_t T, int64_t C);
 size_t layernorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C);
 cudaError_t layernorm_bwd_launch(const ResidualArgs &a, cudaStream_t s);
+// The kernels that hold a row in registers; *G receives the partial rows they write (<= a.G).
+cudaError_t layernorm_bwd_rows_bf16(const ResidualArgs &a, int *G, cudaStream_t s);
+cudaError_t layernorm_bwd_rows_f16(const ResidualArgs &a, int *G, cudaStream_t s);
+cudaError_t layernorm_bwd_rows_f32(const ResidualArgs &a, int *G, cudaStream_t s);
 
 }  // namespace dwk

@@ -12,6 +12,9 @@
 namespace dwk {
 namespace {
 
+// Partial rows: at most two blocks on each of 148 SMs, and at most 64 MiB of them (at least one).
+constexpr int kMaxPartialRows = 296;
+
 // Any C, any alignment: a block per row, two passes over it; the block's partial row lives in the
 // workspace (a thread only touches its own columns, so no synchronization is needed).
 template <typename T>
@@ -67,41 +70,54 @@ layernorm_bwd_general_kernel(const ResidualArgs a) {
     }
 }
 
-// dgamma[c], dbeta[c] = the G partial rows' entries added in order.  A block covers 32 entries of
-// the 2 ceil4(C) with 8 row groups; group r adds rows r, r + 8, ... in order, then the 8 group sums
-// are added in a fixed tree.
+// dgamma[c], dbeta[c] = the G <= 32 R partial rows' entries in a fixed order.  A block covers 32
+// entries of the 2 ceil4(C) (8 lanes of a float4) with 32 row groups; group q adds rows q, q + 32, ...
+// in order, all loads of a thread in flight at once, then the group sums are added in a fixed tree.
+constexpr int kFinalizeRows = (kMaxPartialRows + 31) / 32;
 __global__ void __launch_bounds__(256)
 layernorm_bwd_finalize_kernel(const float *__restrict__ partials, float *__restrict__ dgamma,
                               float *__restrict__ dbeta, int G, int64_t C) {
-    __shared__ float red[8][33];
+    __shared__ float4 red[32][9];
     launch_dependents();
     grid_dependency_wait();
-    const int col = threadIdx.x % 32, rg = threadIdx.x / 32;
-    const int64_t Cp = (C + 3) / 4 * 4, E = 2 * Cp, e = static_cast<int64_t>(blockIdx.x) * 32 + col;
-    const int64_t c = e < Cp ? e : e - Cp;
-    const bool live = e < E && c < C;
-    float s = 0.f;
-    if (live) {
-#pragma unroll 4
-        for (int g = rg; g < G; g += 8) s += __ldg(partials + static_cast<int64_t>(g) * E + e);
+    const int lane = threadIdx.x % 8, q = threadIdx.x / 8;
+    const int64_t Cp = (C + 3) / 4 * 4, E = 2 * Cp, e = static_cast<int64_t>(blockIdx.x) * 32 + lane * 4;
+    float4 v[kFinalizeRows], s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kFinalizeRows; ++i) {
+        const int r = q + 32 * i;
+        v[i] = e < E && r < G ? __ldg(reinterpret_cast<const float4 *>(partials + r * E + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    red[rg][col] = s;
+#pragma unroll
+    for (int i = 0; i < kFinalizeRows; ++i) {
+        s.x += v[i].x;
+        s.y += v[i].y;
+        s.z += v[i].z;
+        s.w += v[i].w;
+    }
+    red[q][lane] = s;
     __syncthreads();
-    if (rg == 0 && live) {
-        const float t = ((red[0][col] + red[1][col]) + (red[2][col] + red[3][col])) +
-                        ((red[4][col] + red[5][col]) + (red[6][col] + red[7][col]));
-        float *o = e < Cp ? dgamma : dbeta;
-        if (o) o[c] = t;
+    if (threadIdx.x < 32) {
+        const float *p = &red[0][0].x + threadIdx.x;
+        float t[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) t[r] = p[r * 36];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+            for (int r = 0; r + d < 32; r += 2 * d) t[r] += t[r + d];
+        const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x, c = o < Cp ? o : o - Cp;
+        float *out = o < Cp ? dgamma : dbeta;
+        if (o < E && c < C && out) out[c] = t[0];
     }
 }
 
 }  // namespace
 
-// One partial row per block; at most 64 MiB of them (and at least one).
 int layernorm_bwd_partial_rows(int64_t B, int64_t T, int64_t C) {
     const int64_t rows = B * T, row_bytes = 2 * ((C + 3) / 4 * 4) * 4;
     int64_t g = (int64_t(64) << 20) / row_bytes;
-    if (g > 256) g = 256;
+    if (g > kMaxPartialRows) g = kMaxPartialRows;
     if (g > rows) g = rows;
     return static_cast<int>(g < 1 ? 1 : g);
 }
@@ -112,17 +128,21 @@ size_t layernorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C) {
 
 // With no rows only the finalize runs, over no partial rows: zeros.
 cudaError_t layernorm_bwd_launch(const ResidualArgs &a, cudaStream_t s) {
-    const bool params = a.dgamma || a.dbeta;
     int G = 0;
     if (a.B * a.T > 0) {
-        G = a.G;
-        const cudaError_t e = with_dtype(a.dtype, [&](auto t) {
-            return launch_programmatic(layernorm_bwd_general_kernel<decltype(t)>, dim3(static_cast<unsigned>(G)),
-                                       dim3(256), 0, s, a);
-        });
+        cudaError_t e = a.dtype == 1   ? layernorm_bwd_rows_bf16(a, &G, s)
+                        : a.dtype == 2 ? layernorm_bwd_rows_f16(a, &G, s)
+                                       : layernorm_bwd_rows_f32(a, &G, s);
+        if (e == cudaErrorNotSupported) {
+            G = a.G;
+            e = with_dtype(a.dtype, [&](auto t) {
+                return launch_programmatic(layernorm_bwd_general_kernel<decltype(t)>, dim3(static_cast<unsigned>(G)),
+                                           dim3(256), 0, s, a);
+            });
+        }
         if (e != cudaSuccess) return e;
     }
-    if (!params) return cudaSuccess;
+    if (!a.dgamma && !a.dbeta) return cudaSuccess;
     const int64_t blocks = (2 * ((a.C + 3) / 4 * 4) + 31) / 32;
     return launch_programmatic(layernorm_bwd_finalize_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
                                static_cast<const float *>(a.partials), a.dgamma, a.dbeta, G, a.C);

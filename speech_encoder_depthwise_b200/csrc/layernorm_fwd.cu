@@ -63,6 +63,10 @@ layernorm_fwd_general_kernel(const ResidualArgs a) {
 }  // namespace
 
 cudaError_t layernorm_fwd_launch(const ResidualArgs &a, cudaStream_t s) {
+    const cudaError_t e = a.dtype == 1   ? layernorm_fwd_rows_bf16(a, s)
+                          : a.dtype == 2 ? layernorm_fwd_rows_f16(a, s)
+                                         : layernorm_fwd_rows_f32(a, s);
+    if (e != cudaErrorNotSupported) return e;
     const int64_t rows = a.B * a.T, most = static_cast<int64_t>(sm_count()) * 8;
     const dim3 grid(static_cast<unsigned>(rows < most ? rows : most));
     return with_dtype(a.dtype, [&](auto t) {
