@@ -151,9 +151,11 @@ def _dev(t, name, dtype=None, shape=None):
 
 
 def _stream(stream):
+    """The raw cudaStream_t of ``stream``; None: the current device's current stream."""
     import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the pointer without a Stream object
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -409,20 +411,25 @@ def dwconv2d_bwd_dw(x, dy, dw, dbias, lengths, stride, pads, workspace, stream=N
 
 
 class _Operands:
-    """Checks the tensors of one call and gives their pointers.  All of them live on the first
-    one's device; ``call`` runs there, on ``stream`` or that device's current stream."""
+    """Checks the tensors of one call against the first one, [B, T, C], and gives their pointers.
+    All of them live on that one's device; ``call`` runs there, on ``stream`` or the device's
+    current stream."""
 
-    __slots__ = ("dev", "dtype", "shape", "B", "C", "code", "f32")
+    __slots__ = ("dev", "dtype", "shape", "rows", "chan", "items", "code", "f32", "i32", "i64", "first")
 
     def __init__(self, x, name):
         import torch
         if not x.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if x.dim() != 3:
-            raise ValueError(f"{name} must have shape [B, T, C], got {tuple(x.shape)}")
-        self.dev, self.dtype, self.shape = x.get_device(), x.dtype, x.shape
-        self.B, _, self.C = self.shape
-        self.code, self.f32 = _dtype_code(x), torch.float32
+        self.shape = shape = tuple(x.shape)
+        if len(shape) != 3:
+            raise ValueError(f"{name} must have shape [B, T, C], got {shape}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        self.dev, self.dtype, self.first = x.get_device(), x.dtype, x.data_ptr()
+        self.rows, self.chan, self.items = shape[:2], shape[2:], shape[:1]
+        self.code = _dtype_code(x)
+        self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
 
     def ptr(self, t, name, dtype, shape):
         if t is None:
@@ -432,27 +439,10 @@ class _Operands:
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
-
-    def act(self, t, name):
-        return self.ptr(t, name, self.dtype, self.shape)
-
-    def row(self, t, name):
-        return self.ptr(t, name, self.f32, self.shape[:2])
-
-    def chan(self, t, name):
-        return self.ptr(t, name, self.f32, self.shape[2:])
-
-    def lengths(self, t):
-        import torch
-        return self.ptr(t, "lengths", torch.int32, self.shape[:1])
-
-    def rng(self, t):
-        import torch
-        return self.ptr(t, "rng", torch.int64, (2,))
 
     def workspace(self, t):
         if t is None:
@@ -461,12 +451,11 @@ class _Operands:
 
     def call(self, fn, stream, *args):
         import torch
-        handle = getattr(lib(), fn)
         if self.dev == torch.cuda.current_device():
-            st = handle(*args, _stream(stream))
+            st = getattr(_lib or lib(), fn)(*args, _stream(stream))
         else:
             with torch.cuda.device(self.dev):
-                st = handle(*args, _stream(stream))
+                st = getattr(lib(), fn)(*args, _stream(stream))
         if st != DW_OK:
             raise DwError(fn, st)
 
@@ -475,8 +464,10 @@ def dw_layernorm_fwd(x, gamma, beta, y, mean, rstd, lengths, eps=1e-5, stream=No
     """y = layer norm of x over C on the valid frames (zeros elsewhere); gamma, beta, mean and rstd
     may be None."""
     o = _Operands(x, "x")
-    o.call("dw_layernorm_fwd", stream, o.act(x, "x"), o.chan(gamma, "gamma"), o.chan(beta, "beta"), o.act(y, "y"),
-           o.row(mean, "mean"), o.row(rstd, "rstd"), o.lengths(lengths), *o.shape, eps, o.code)
+    ptr, f32 = o.ptr, o.f32
+    o.call("dw_layernorm_fwd", stream, o.first, ptr(gamma, "gamma", f32, o.chan), ptr(beta, "beta", f32, o.chan),
+           ptr(y, "y", o.dtype, o.shape), ptr(mean, "mean", f32, o.rows), ptr(rstd, "rstd", f32, o.rows),
+           ptr(lengths, "lengths", o.i32, o.items), *o.shape, eps, o.code)
 
 
 def dw_layernorm_bwd_workspace_size(B, T, C) -> int:
@@ -487,24 +478,29 @@ def dw_layernorm_bwd_workspace_size(B, T, C) -> int:
 def dw_layernorm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, lengths, workspace, stream=None):
     """Gradients of ``dw_layernorm_fwd`` into dx and (float32 [C], either may be None) dgamma, dbeta."""
     o = _Operands(x, "x")
-    o.call("dw_layernorm_bwd", stream, o.act(x, "x"), o.act(dy, "dy"), o.chan(gamma, "gamma"), o.row(mean, "mean"),
-           o.row(rstd, "rstd"), o.act(dx, "dx"), o.chan(dgamma, "dgamma"), o.chan(dbeta, "dbeta"), o.lengths(lengths),
-           *o.shape, o.code, *o.workspace(workspace))
+    ptr, f32 = o.ptr, o.f32
+    o.call("dw_layernorm_bwd", stream, o.first, ptr(dy, "dy", o.dtype, o.shape), ptr(gamma, "gamma", f32, o.chan),
+           ptr(mean, "mean", f32, o.rows), ptr(rstd, "rstd", f32, o.rows), ptr(dx, "dx", o.dtype, o.shape),
+           ptr(dgamma, "dgamma", f32, o.chan), ptr(dbeta, "dbeta", f32, o.chan),
+           ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code, *o.workspace(workspace))
 
 
 def dw_dropout_add_fwd(x, residual, y, rng, p, alpha, lengths, stream=None):
     """y = residual + alpha/(1-p) x on the kept elements of the valid frames, residual alone on the
     dropped ones (residual may be None); ``rng`` is a CUDA int64 tensor {seed, offset}."""
     o = _Operands(x, "x")
-    o.call("dw_dropout_add_fwd", stream, o.act(x, "x"), o.act(residual, "residual"), o.act(y, "y"), o.rng(rng), p,
-           alpha, o.lengths(lengths), *o.shape, o.code)
+    ptr = o.ptr
+    o.call("dw_dropout_add_fwd", stream, o.first, ptr(residual, "residual", o.dtype, o.shape),
+           ptr(y, "y", o.dtype, o.shape), ptr(rng, "rng", o.i64, (2,)), p, alpha,
+           ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code)
 
 
 def dw_dropout_add_bwd(dy, dx, rng, p, alpha, lengths, stream=None):
     """Gradient of ``dw_dropout_add_fwd`` with respect to x (same rng, p and alpha) into dx."""
     o = _Operands(dy, "dy")
-    o.call("dw_dropout_add_bwd", stream, o.act(dy, "dy"), o.act(dx, "dx"), o.rng(rng), p, alpha, o.lengths(lengths),
-           *o.shape, o.code)
+    ptr = o.ptr
+    o.call("dw_dropout_add_bwd", stream, o.first, ptr(dx, "dx", o.dtype, o.shape), ptr(rng, "rng", o.i64, (2,)), p,
+           alpha, ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code)
 
 
 def dw_dropout_add_layernorm_fwd(x, residual, rng, p, alpha, gamma, beta, h, y, mean, rstd, lengths, eps=1e-5,
@@ -512,9 +508,11 @@ def dw_dropout_add_layernorm_fwd(x, residual, rng, p, alpha, gamma, beta, h, y, 
     """h = ``dw_dropout_add_fwd``'s sum and y = its layer norm in one pass (residual, h, mean, rstd,
     gamma and beta may be None)."""
     o = _Operands(x, "x")
-    o.call("dw_dropout_add_layernorm_fwd", stream, o.act(x, "x"), o.act(residual, "residual"), o.rng(rng), p, alpha,
-           o.chan(gamma, "gamma"), o.chan(beta, "beta"), o.act(h, "h"), o.act(y, "y"), o.row(mean, "mean"),
-           o.row(rstd, "rstd"), o.lengths(lengths), *o.shape, eps, o.code)
+    ptr, f32 = o.ptr, o.f32
+    o.call("dw_dropout_add_layernorm_fwd", stream, o.first, ptr(residual, "residual", o.dtype, o.shape),
+           ptr(rng, "rng", o.i64, (2,)), p, alpha, ptr(gamma, "gamma", f32, o.chan), ptr(beta, "beta", f32, o.chan),
+           ptr(h, "h", o.dtype, o.shape), ptr(y, "y", o.dtype, o.shape), ptr(mean, "mean", f32, o.rows),
+           ptr(rstd, "rstd", f32, o.rows), ptr(lengths, "lengths", o.i32, o.items), *o.shape, eps, o.code)
 
 
 def dw_dropout_add_layernorm_bwd(dy, dh, h, gamma, mean, rstd, rng, p, alpha, dx, dresidual, dgamma, dbeta, lengths,
@@ -522,10 +520,13 @@ def dw_dropout_add_layernorm_bwd(dy, dh, h, gamma, mean, rstd, rng, p, alpha, dx
     """Gradients of ``dw_dropout_add_layernorm_fwd`` from dy and dh (None: zeros) into dx, dresidual
     and (float32 [C]) dgamma, dbeta; dresidual, dgamma and dbeta may be None."""
     o = _Operands(dy, "dy")
-    o.call("dw_dropout_add_layernorm_bwd", stream, o.act(dy, "dy"), o.act(dh, "dh"), o.act(h, "h"),
-           o.chan(gamma, "gamma"), o.row(mean, "mean"), o.row(rstd, "rstd"), o.rng(rng), p, alpha, o.act(dx, "dx"),
-           o.act(dresidual, "dresidual"), o.chan(dgamma, "dgamma"), o.chan(dbeta, "dbeta"), o.lengths(lengths),
-           *o.shape, o.code, *o.workspace(workspace))
+    ptr, f32 = o.ptr, o.f32
+    o.call("dw_dropout_add_layernorm_bwd", stream, o.first, ptr(dh, "dh", o.dtype, o.shape),
+           ptr(h, "h", o.dtype, o.shape), ptr(gamma, "gamma", f32, o.chan), ptr(mean, "mean", f32, o.rows),
+           ptr(rstd, "rstd", f32, o.rows), ptr(rng, "rng", o.i64, (2,)), p, alpha, ptr(dx, "dx", o.dtype, o.shape),
+           ptr(dresidual, "dresidual", o.dtype, o.shape), ptr(dgamma, "dgamma", f32, o.chan),
+           ptr(dbeta, "dbeta", f32, o.chan), ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code,
+           *o.workspace(workspace))
 
 
 def dw_selftest_wait_timeout(done, stream=None):

@@ -96,13 +96,13 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float f[8] = {}, q[8] = {};
+        float2 f[4] = {}, q[4] = {};
         if (st[u] == kValid) {
             xo[u].get(f);
             if constexpr (RES) ro[u].get(q);
             if constexpr (DROP) D.apply(static_cast<uint64_t>(mine + u * kStep) >> 3, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = RES ? fmaf(mult, f[i], q[i]) : mult * f[i];
+            for (int i = 0; i < 4; ++i) f[i] = RES ? ffma2(both(mult), f[i], q[i]) : fmul2(both(mult), f[i]);
         }
         if (st[u] <= kMasked) Oct<T>::store(y + mine + u * kStep, f);
     }
@@ -113,7 +113,7 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
     for (int u = 0; mixed; ++u, mixed >>= 1) {
         if (!(mixed & 1u)) continue;
         const int64_t e0 = mine + u * kStep;
-        float keep[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+        float2 keep[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
         if constexpr (DROP) D.apply(static_cast<uint64_t>(e0) >> 3, keep);
         int64_t item = lengths ? item_of(e0) : 0, next = lengths ? (item + 1) * TC : N;
         int64_t lim = lengths ? item * TC + clamp_len(lengths, item, Tn) * C : N;
@@ -128,7 +128,7 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
             float v = 0.f;
             if (e < lim) {
                 if constexpr (RES) v = load1(res + e);
-                if (keep[i] != 0.f) v = fmaf(mult, load1(x + e), v);
+                if ((i % 2 ? keep[i / 2].y : keep[i / 2].x) != 0.f) v = fmaf(mult, load1(x + e), v);
             }
             store1(y + e, v);
         }

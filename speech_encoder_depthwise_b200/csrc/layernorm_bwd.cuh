@@ -10,47 +10,47 @@ namespace lnb {
 
 // TPR threads hold a row's NO octets each in registers.  Every thread keeps its channels from row to
 // row, so dgamma and dbeta add up in registers over all its rows; the block's groups are then added
-// in a fixed order through shared memory into the block's partial row.
+// in a fixed order through shared memory into the block's partial row.  SHIFT: rows that do not
+// start on an octet (C not a multiple of 8).
 template <typename T, int TPR, int NO, int THREADS, bool SHIFT, bool DROP>
 __global__ void __launch_bounds__(THREADS)
 layernorm_bwd_rows_kernel(const ResidualArgs a) {
-    constexpr int GPB = THREADS / TPR, W = THREADS / 32;
+    constexpr int GPB = THREADS / TPR, W = THREADS / 32, HALF = W / 2;
     __shared__ float2 red[2 * (TPR > 32 ? TPR / 32 : 1)];
-    extern __shared__ float sp[];  // SHIFT: gamma, padded; at the end the warps' dgamma, dbeta
+    extern __shared__ float sp[];  // SHIFT: gamma; at the end the warps' dgamma, dbeta
     launch_dependents();
-    const int lane = threadIdx.x % TPR, g = threadIdx.x / TPR;
+    const int g = threadIdx.x / TPR, grid = gridDim.x, rows = static_cast<int>(a.B * a.T);
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy), *dh = static_cast<const T *>(a.dh);
     T *dx = static_cast<T *>(a.dx), *dres = static_cast<T *>(a.dres);
-    const int64_t N = a.B * a.T * a.C, grid = gridDim.x;
-    const int C = static_cast<int>(a.C);
+    Channels<T, TPR, NO, SHIFT> ch;
+    ch.lane = threadIdx.x % TPR;
+    ch.C = static_cast<int>(a.C);
+    ch.N = rows * a.C;
+    const int first = blockIdx.x + grid * g, Q = shifted_q(ch.C);
+    ch.s = SHIFT ? static_cast<int>((first * a.C) % 8) : 0;
+    int off[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) off[i] = shifted_off(i, ch.s, Q) + ch.lane;
     grid_dependency_wait();
     if constexpr (SHIFT) {
-        for (int c = threadIdx.x; c < C; c += THREADS) sp[pad32(c)] = a.gamma ? __ldg(a.gamma + c) : 1.f;
+        for (int i = threadIdx.x; i < 8 * Q; i += THREADS) {
+            const int c = i / Q + 8 * (i % Q - 1);
+            sp[i] = c < 0 || c >= ch.C ? 0.f : a.gamma ? __ldg(a.gamma + c) : 1.f;
+        }
         __syncthreads();
     }
     Dropper D;
     if constexpr (DROP) D.start(a.rng, a.thr);
-    RowWalk w;
-    w.start(a.lengths, blockIdx.x + grid * g, grid * GPB, a.B, a.T);
-    const int s = SHIFT ? static_cast<int>((w.r * a.C) % 8) : 0;
-    const float inv = 1.f / static_cast<float>(C);
+    const float inv = 1.f / static_cast<float>(ch.C);
     int flip = 0;
-    float ag[NO][8] = {}, ab[NO][8] = {};
-    // groups of one warp walk together (their sums share its shuffles)
-    const int64_t lead = TPR < 32 ? blockIdx.x + grid * (threadIdx.x / 32 * (32 / TPR)) : 0;
-    for (int64_t k = 0; TPR < 32 ? lead + k * w.step < w.rows : w.in(); ++k, w.next()) {
-        const bool live = TPR < 32 ? (w.in() && w.valid()) : w.valid();
-        if (TPR >= 32 ? !live : (w.in() && !live)) {
-            const float zero[8] = {};
-#pragma unroll
-            for (int j = 0; j < NO; ++j) {
-                const OctAt<T, SHIFT> at(w.r, a.C, j * TPR + lane, s);
-                if (!at.any()) continue;
-                at.store(dx, zero);
-                if (dres) at.store(dres, zero);
-            }
-            if (TPR >= 32) continue;
-        }
+    float2 ag[NO][4] = {}, ab[NO][4] = {};
+    RowWalk w;
+    w.start(a.lengths, first, grid * GPB, rows, static_cast<int>(a.T));
+    // groups of one warp walk together (their sums share its shuffles): until the first one is done
+    int lead = TPR < 32 ? blockIdx.x + grid * (threadIdx.x / 32 * (32 / TPR)) : first;
+    for (; lead < rows; lead += w.step, w.next()) {
+        const bool in = w.in(), live = in && w.valid();
+        const int64_t e = ch.at(w.r);
         Oct<T> xo[NO], go[NO], ho[NO];
         float mean = 0.f, rstd = 0.f;
         if (live) {
@@ -59,123 +59,118 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            const OctAt<T, SHIFT> at(w.r, a.C, j * TPR + lane, s);
             xo[j].zero();
             go[j].zero();
             ho[j].zero();
-            if (live && at.any()) {
-                at.load(x, xo[j], N);
-                at.load(dy, go[j], N);
-                if (dh) at.load(dh, ho[j], N);
+            if (!live || !ch.any(j)) continue;
+            ch.load(x, e, j, xo[j]);
+            ch.load(dy, e, j, go[j]);
+            if (dh) ch.load(dh, e, j, ho[j]);
+        }
+        if (in && !live) {
+            const float2 zero[4] = {};
+#pragma unroll
+            for (int j = 0; j < NO; ++j) {
+                if (!ch.any(j)) continue;
+                ch.store(dx, e, j, zero);
+                if (dres) ch.store(dres, e, j, zero);
             }
         }
-        float2 sum = make_float2(0.f, 0.f);
-        float gg[NO][8];
+        if (TPR >= 32 && !live) continue;
+        float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+        float2 gg[NO][4];
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            const OctAt<T, SHIFT> at(w.r, a.C, j * TPR + lane, s);
-            if (!at.any()) continue;
-            float f[8], ga[8];
+            if (!ch.any(j)) continue;
+            float2 f[4], ga[4];
             xo[j].get(f);
             go[j].get(gg[j]);
             if constexpr (SHIFT) {
+                ch.clear_outside(j, f);
+                ch.clear_outside(j, gg[j]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ga[i] = sp[at.has(i) ? pad32(at.c0 + i) : 0];
-                    f[i] = at.has(i) ? f[i] : 0.f;
-                    gg[j][i] = at.has(i) ? gg[j][i] : 0.f;
-                }
+                for (int i = 0; i < 4; ++i) ga[i] = make_float2(sp[off[2 * i] + j * TPR], sp[off[2 * i + 1] + j * TPR]);
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const float4 p = a.gamma ? __ldg(reinterpret_cast<const float4 *>(a.gamma + at.c0 + i)) : make_float4(1.f, 1.f, 1.f, 1.f);
-                    ga[i] = p.x; ga[i + 1] = p.y; ga[i + 2] = p.z; ga[i + 3] = p.w;
-                }
+                load_params8(a.gamma ? a.gamma + ch.c0(j) : nullptr, 1.f, ga);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xh = (f[i] - mean) * rstd, d = gg[j][i];
-                ag[j][i] = fmaf(d, xh, ag[j][i]);
-                ab[j][i] += d;
-                gg[j][i] = d * ga[i];
-                sum.x += gg[j][i];
-                sum.y = fmaf(gg[j][i], xh, sum.y);
+            for (int i = 0; i < 4; ++i) {
+                const float2 xh = fmul2(fadd2(f[i], both(-mean)), both(rstd));
+                ag[j][i] = ffma2(gg[j][i], xh, ag[j][i]);
+                ab[j][i] = fadd2(ab[j][i], gg[j][i]);
+                gg[j][i] = fmul2(gg[j][i], ga[i]);
+                s1 = fadd2(s1, gg[j][i]);
+                s2 = ffma2(gg[j][i], xh, s2);
             }
         }
-        sum = row_sum2<TPR>(sum, red, flip);
+        const float2 sum = row_sum<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red, flip);
         const float c1 = sum.x * inv, c2 = sum.y * inv;
+        if (!live) continue;
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            const OctAt<T, SHIFT> at(w.r, a.C, j * TPR + lane, s);
-            if (!at.any() || !live) continue;
-            float f[8], d[8];
+            if (!ch.any(j)) continue;
+            float2 f[4], d[4];
             xo[j].get(f);
             ho[j].get(d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xh = (f[i] - mean) * rstd;
-                f[i] = fmaf(rstd, gg[j][i] - fmaf(xh, c2, c1), d[i]);
+            for (int i = 0; i < 4; ++i) {
+                const float2 xh = fmul2(fadd2(f[i], both(-mean)), both(rstd));
+                f[i] = ffma2(both(rstd), fadd2(gg[j][i], ffma2(xh, both(-c2), both(-c1))), d[i]);
             }
-            if (dres) at.store(dres, f);
-            if constexpr (DROP) D.apply(static_cast<uint64_t>(at.e0) >> 3, f);
+            if (dres) ch.store(dres, e, j, f);
+            if constexpr (DROP) D.apply(static_cast<uint64_t>(e + 8 * j * TPR) >> 3, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= a.mult;
-            at.store(dx, f);
+            for (int i = 0; i < 4; ++i) f[i] = fmul2(f[i], both(a.mult));
+            ch.store(dx, e, j, f);
         }
     }
     if (!a.dgamma && !a.dbeta) return;
+    // a warp's or block's sums by channel, in the shifted layout: dgamma at slot[at], dbeta at slot[8 Q + at]
     const int64_t Cp = (a.C + 3) / 4 * 4;
     float *pg = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * Cp;
     if constexpr (TPR > 32) {  // one group: its channels straight to the partial row
 #pragma unroll
-        for (int j = 0; j < NO; ++j) {
-            const OctAt<T, SHIFT> at(0, a.C, j * TPR + lane, s);
+        for (int j = 0; j < NO; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (at.any() && at.has(i)) {
-                    pg[at.c0 + i] = ag[j][i];
-                    pg[Cp + at.c0 + i] = ab[j][i];
+                if (ch.any(j) && ch.has(j, i)) {
+                    pg[ch.c0(j) + i] = i % 2 ? ag[j][i / 2].y : ag[j][i / 2].x;
+                    pg[Cp + ch.c0(j) + i] = i % 2 ? ab[j][i / 2].y : ab[j][i / 2].x;
                 }
-        }
     } else {
-        if constexpr (TPR < 32) {  // the warp's groups hold the same channels (no SHIFT here)
-#pragma unroll
-            for (int o = TPR; o < 32; o <<= 1)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ag[0][i] += __shfl_xor_sync(0xffffffffu, ag[0][i], o);
-                    ab[0][i] += __shfl_xor_sync(0xffffffffu, ab[0][i], o);
-                }
-        }
-        // warps HALF .. W-1 store, warps 0 .. HALF-1 add to them, then the HALF slots are added in order
-        constexpr int HALF = W / 2;
-        const int P = pad32(C - 1) + 1, warp = threadIdx.x / 32;
-        if constexpr (SHIFT) __syncthreads();  // gamma is no longer read
-#pragma unroll
+        // warps HALF .. W-1 store, warps 0 .. HALF-1 add to them, then the HALF slots are added in
+        // order; the groups of one warp take turns
+        const int warp = threadIdx.x / 32;
+        __syncthreads();  // SHIFT: gamma is no longer read
+#pragma unroll 1
         for (int phase = 0; phase < 2; ++phase) {
-            float *slot = sp + (phase == 0 ? warp - HALF : warp) * 2 * P;
-            if ((phase == 0) == (warp >= HALF) && (TPR == 32 || threadIdx.x % 32 < TPR)) {
+            float *slot = sp + (phase == 0 ? warp - HALF : warp) * 16 * Q;
+#pragma unroll 1
+            for (int turn = 0; turn < 32 / TPR; ++turn) {
+                const bool add = phase > 0 || turn > 0;
+                if ((phase == 0) == (warp >= HALF) && static_cast<int>(threadIdx.x % 32) / TPR == turn) {
 #pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                    const OctAt<T, SHIFT> at(0, a.C, j * TPR + lane, s);
+                    for (int j = 0; j < NO; ++j)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (at.any() && at.has(i)) {
-                            const int c = pad32(at.c0 + i);
-                            slot[c] = phase == 0 ? ag[j][i] : slot[c] + ag[j][i];
-                            slot[P + c] = phase == 0 ? ab[j][i] : slot[P + c] + ab[j][i];
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            if (ch.any(j) && ch.has(j, i)) {
+                                float *p = slot + off[i] + j * TPR;
+                                const float vg = i % 2 ? ag[j][i / 2].y : ag[j][i / 2].x, vb = i % 2 ? ab[j][i / 2].y : ab[j][i / 2].x;
+                                p[0] = add ? p[0] + vg : vg;
+                                p[8 * Q] = add ? p[8 * Q] + vb : vb;
+                            }
                 }
+                __syncwarp();
             }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < 2 * C; c += THREADS) {
-            const int which = c >= C, ch = which ? c - C : c;
-            const float *p = sp + which * P + pad32(ch);
+        for (int c = threadIdx.x; c < 2 * ch.C; c += THREADS) {
+            const int which = c >= ch.C, k = which ? c - ch.C : c;
+            const float *p = sp + which * 8 * Q + (k % 8) * Q + k / 8 + 1;
             float t = p[0];
 #pragma unroll
-            for (int q = 1; q < HALF; ++q) t += p[q * 2 * P];
-            pg[which * Cp + ch] = t;
+            for (int q = 1; q < HALF; ++q) t += p[q * 16 * Q];
+            pg[which * Cp + k] = t;
         }
     }
 }
@@ -184,12 +179,12 @@ template <typename T, int TPR, int NO, int THREADS, bool SHIFT, bool DROP>
 cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     constexpr int GPB = THREADS / TPR, HALF = THREADS / 64;
     const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, THREADS, SHIFT, DROP>;
-    const size_t P = static_cast<size_t>((a.C - 1) + ((a.C - 1) >> 5) + 1);
-    size_t smem = SHIFT ? P * sizeof(float) : 0;
-    if (TPR <= 32) smem = HALF * 2 * P * sizeof(float);
+    const size_t words = 8 * static_cast<size_t>((a.C + 7) / 8 + 2);
+    size_t smem = SHIFT ? words * sizeof(float) : 0;
+    if (TPR <= 32) smem = HALF * 2 * words * sizeof(float);
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    constexpr int kPerSm = TPR == 256 || (TPR == 512 && NO == 1) ? 2 : 1;
+    constexpr int kPerSm = THREADS <= 256 && TPR > 32 && NO <= 2 ? 2 : 1;
     const int64_t rows = a.B * a.T;
     int64_t grid = sm_count() * kPerSm;
     if (grid > a.G) grid = a.G;
@@ -215,33 +210,27 @@ cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     return a.thr ? launch<T, TPR, NO, kThreads, SHIFT, true>(a, G, s) : launch<T, TPR, NO, kThreads, SHIFT, false>(a, G, s);
 }
 
+template <typename T, bool SHIFT>
+cudaError_t launch_octets(const ResidualArgs &a, int64_t n, int *G, cudaStream_t s) {
+    if (n <= 8) return launch<T, 8, 1, SHIFT>(a, G, s);
+    if (n <= 16) return launch<T, 8, 2, SHIFT>(a, G, s);
+    if (n <= 32) return launch<T, 16, 2, SHIFT>(a, G, s);
+    if (n <= 64) return launch<T, 32, 2, SHIFT>(a, G, s);
+    if (n <= 96) return launch<T, 32, 3, SHIFT>(a, G, s);
+    if (n <= 128) return launch<T, 32, 4, SHIFT>(a, G, s);
+    if (n <= 160) return launch<T, 32, 5, SHIFT>(a, G, s);
+    if (n <= 256) return launch<T, 256, 1, SHIFT>(a, G, s);
+    if (n <= 512) return launch<T, 256, 2, SHIFT>(a, G, s);
+    if (n <= 1024) return launch<T, 512, 2, SHIFT>(a, G, s);
+    return cudaErrorNotSupported;
+}
+
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, int *G, cudaStream_t s) {
-    if (!a.vec_oct || a.C > 8192) return cudaErrorNotSupported;
-    if (a.C % 8 == 0 && reinterpret_cast<uintptr_t>(a.gamma) % 16 == 0) {
-        const int64_t n = a.C / 8;
-        if (n <= 8) return launch<T, 8, 1, false>(a, G, s);
-        if (n <= 16) return launch<T, 16, 1, false>(a, G, s);
-        if (n <= 32) return launch<T, 32, 1, false>(a, G, s);
-        if (n <= 64) return launch<T, 32, 2, false>(a, G, s);
-        if (n <= 96) return launch<T, 32, 3, false>(a, G, s);
-        if (n <= 128) return launch<T, 32, 4, false>(a, G, s);
-        if (n <= 160) return launch<T, 32, 5, false>(a, G, s);
-        if (n <= 256) return launch<T, 256, 1, false>(a, G, s);
-        if (n <= 512) return launch<T, 512, 1, false>(a, G, s);
-        return launch<T, 512, 2, false>(a, G, s);
-    }
-    const int64_t n = (a.C + 14) / 8;  // octets a row may touch: up to 7 elements before its first
-    if (n <= 32) return launch<T, 32, 1, true>(a, G, s);
-    if (n <= 64) return launch<T, 32, 2, true>(a, G, s);
-    if (n <= 96) return launch<T, 32, 3, true>(a, G, s);
-    if (n <= 128) return launch<T, 32, 4, true>(a, G, s);
-    if (n <= 160) return launch<T, 32, 5, true>(a, G, s);
-    if (n <= 256) return launch<T, 256, 1, true>(a, G, s);
-    if (n <= 512) return launch<T, 512, 1, true>(a, G, s);
-    if (n <= 1024) return launch<T, 512, 2, true>(a, G, s);
-    return cudaErrorNotSupported;
+    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30)) return cudaErrorNotSupported;
+    if (a.C % 8 == 0 && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0) return launch_octets<T, false>(a, a.C / 8, G, s);
+    return launch_octets<T, true>(a, (a.C + 14) / 8, G, s);  // a row may touch 7 elements before its first
 }
 
 }  // namespace lnb

@@ -19,6 +19,10 @@ template <typename T> __device__ __forceinline__ void store1(T *p, float v) {
     Vec<T, 1>::store(p, f);
 }
 
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Eight consecutive elements, moved with one instruction (16 bytes of a 16-bit type, 32 of float32):
 // the unit of the row kernels, and one block of the dropout generator.  Loads do not allocate in
 // L1 (every activation is read once), which leaves it to gamma and beta.
@@ -30,19 +34,14 @@ template <typename T> struct Oct {
                      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
     }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = H::unpack(w[i]);
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
-        }
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        f[0] = H::unpack(r.x); f[1] = H::unpack(r.y); f[2] = H::unpack(r.z); f[3] = H::unpack(r.w);
     }
-    __device__ __forceinline__ void set(const float (&f)[8]) {
-        r = make_uint4(H::pack(f[0], f[1]), H::pack(f[2], f[3]), H::pack(f[4], f[5]), H::pack(f[6], f[7]));
+    __device__ __forceinline__ void set(const float2 (&f)[4]) {
+        r = make_uint4(H::pack(f[0].x, f[0].y), H::pack(f[1].x, f[1].y), H::pack(f[2].x, f[2].y),
+                       H::pack(f[3].x, f[3].y));
     }
-    static __device__ __forceinline__ void store(T *p, const float (&f)[8]) {
+    static __device__ __forceinline__ void store(T *p, const float2 (&f)[4]) {
         Oct o;
         o.set(f);
         *reinterpret_cast<uint4 *>(p) = o.r;
@@ -50,93 +49,115 @@ template <typename T> struct Oct {
 };
 
 template <> struct Oct<float> {
-    float v[8];
+    float2 v[4];
     __device__ __forceinline__ void load(const float *p) {
         asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y),
+                       "=f"(v[3].x), "=f"(v[3].y)
                      : "l"(p) : "memory");
     }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = v[i];
-    }
-    __device__ __forceinline__ void set(const float (&f)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = f[i];
-    }
-    static __device__ __forceinline__ void store(float *p, const float (&f)[8]) {
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]),
-                     "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+    __device__ __forceinline__ void zero() { v[0] = v[1] = v[2] = v[3] = make_float2(0.f, 0.f); }
+    __device__ __forceinline__ void get(float2 (&f)[4]) const { f[0] = v[0]; f[1] = v[1]; f[2] = v[2]; f[3] = v[3]; }
+    __device__ __forceinline__ void set(const float2 (&f)[4]) { v[0] = f[0]; v[1] = f[1]; v[2] = f[2]; v[3] = f[3]; }
+    static __device__ __forceinline__ void store(float *p, const float2 (&f)[4]) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0].x), "f"(f[0].y),
+                     "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y)
                      : "memory");
     }
 };
 
-// Octet v of row r in a row kernel.  Octets lie on multiples of 8 of the flat index, so that every
-// one is an aligned word whatever C is: row r starts s = (r C) mod 8 elements into its first octet,
-// and octet v holds its channels 8 v - s .. 8 v - s + 7.  SHIFT false: C is a multiple of 8, s = 0.
-// A thread's rows are a multiple of 8 apart, so it keeps its s and its channels.
-template <typename T, bool SHIFT> struct OctAt {
-    int64_t e0;  // flat index of its first element
-    int c0;      // channel of its first element (may be negative)
-    int C;
-    __device__ __forceinline__ OctAt(int64_t r, int64_t C_, int v, int s)
-        : e0(r * C_ + (8 * v - s)), c0(8 * v - s), C(static_cast<int>(C_)) {}
-    __device__ __forceinline__ bool any() const { return c0 < C; }
-    __device__ __forceinline__ bool has(int i) const { return !SHIFT || static_cast<unsigned>(c0 + i) < static_cast<unsigned>(C); }
-    __device__ __forceinline__ bool full() const { return !SHIFT || (c0 >= 0 && c0 + 8 <= C); }
-    // Neighbouring rows' elements come along and are ignored; only the last octet of a tensor of N
-    // elements may reach past it.
-    __device__ __forceinline__ void load(const T *p, Oct<T> &o, int64_t N) const {
-        if (!SHIFT || e0 + 8 <= N) {
-            o.load(p + e0);
+// Eight float32 parameters (32-byte aligned), kept in L1 for the rows to come; `missing` without any.
+__device__ __forceinline__ void load_params8(const float *p, float missing, float2 (&f)[4]) {
+    if (p == nullptr) {
+        f[0] = f[1] = f[2] = f[3] = both(missing);
+        return;
+    }
+    asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y), "=f"(f[2].x), "=f"(f[2].y), "=f"(f[3].x),
+                   "=f"(f[3].y)
+                 : "l"(p) : "memory");
+}
+
+// The channels of one thread in a row kernel: NO octets, TPR apart, of a row held by TPR threads.
+// Octets lie on multiples of 8 of the flat index, so every one is an aligned word whatever C is: a row
+// starts s = (r C) mod 8 elements into its first octet, and octet v holds its channels 8 v - s ..
+// 8 v - s + 7.  SHIFT false: C is a multiple of 8, s = 0.  A thread's rows are a multiple of 8
+// apart, so it keeps its s and its channels.
+template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
+    int lane, s, C;
+    int64_t N;  // elements of the tensor
+    __device__ __forceinline__ int c0(int j) const { return 8 * (j * TPR + lane) - s; }
+    __device__ __forceinline__ bool any(int j) const { return c0(j) < C; }
+    __device__ __forceinline__ bool full(int j) const { return !SHIFT || (c0(j) >= 0 && c0(j) + 8 <= C); }
+    __device__ __forceinline__ bool has(int j, int i) const {
+        return !SHIFT || static_cast<unsigned>(c0(j) + i) < static_cast<unsigned>(C);
+    }
+    // Flat index of the thread's first octet in row r.
+    __device__ __forceinline__ int64_t at(int64_t r) const { return r * C - s + 8 * lane; }
+    // Octet j, e = at(r).  Neighbouring rows' elements come along in a row's first and last octet and
+    // are ignored; only the last octet of the tensor may reach past it.
+    __device__ __forceinline__ void load(const T *p, int64_t e, int j, Oct<T> &o) const {
+        const int64_t ej = e + 8 * j * TPR;
+        if (full(j) || ej + 8 <= N) {
+            o.load(p + ej);
         } else {
-            float f[8];
+            float2 f[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = has(i) ? load1(p + e0 + i) : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                f[i].x = has(j, 2 * i) ? load1(p + ej + 2 * i) : 0.f;
+                f[i].y = has(j, 2 * i + 1) ? load1(p + ej + 2 * i + 1) : 0.f;
+            }
             o.set(f);
         }
     }
-    __device__ __forceinline__ void store(T *p, const float (&f)[8]) const {
-        if (full()) {
-            Oct<T>::store(p + e0, f);
+    __device__ __forceinline__ void store(T *p, int64_t e, int j, const float2 (&f)[4]) const {
+        T *q = p + e + 8 * j * TPR;
+        if (full(j)) {
+            Oct<T>::store(q, f);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (has(i)) store1(p + e0 + i, f[i]);
+            for (int i = 0; i < 4; ++i) {
+                if (has(j, 2 * i)) store1(q + 2 * i, f[i].x);
+                if (has(j, 2 * i + 1)) store1(q + 2 * i + 1, f[i].y);
+            }
+        }
+    }
+    // Zeros in the places of a partial octet that are not this row's.
+    __device__ __forceinline__ void clear_outside(int j, float2 (&f)[4]) const {
+        if (full(j)) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!has(j, 2 * i)) f[i].x = 0.f;
+            if (!has(j, 2 * i + 1)) f[i].y = 0.f;
         }
     }
 };
 
-// The rows of one thread group, k-th row blk + grid (g + groups k), and whether each is valid.
+// Parameters in shared memory for rows that start inside an octet: channel c at word
+// (c % 8) Q + c / 8 + 1.  Element i of octet v is channel 8 v + i - s, at v + off(i) with off the
+// same in every octet, so the lanes of a row read neighbouring words: no bank conflicts, and no
+// address arithmetic but an immediate.  Places without a channel hold zeros.
+__device__ __forceinline__ int shifted_q(int C) { return (C + 7) / 8 + 2; }
+__device__ __forceinline__ int shifted_off(int i, int s, int Q) { return ((i - s) & 7) * Q + (i < s ? 0 : 1); }
+
+// The rows of one thread group: first, first + step, ..., and whether each is valid (32-bit rows).
 struct RowWalk {
-    int64_t r, rows, step;
-    int64_t b, t, db, dt, T;
+    int r, rows, step, t, b, dt, db, T, len;
     const int32_t *lengths;
-    __device__ __forceinline__ void start(const int32_t *lengths_, int64_t first, int64_t step_, int64_t B, int64_t T_) {
-        r = first;
-        rows = B * T_;
-        step = step_;
-        lengths = lengths_;
-        T = T_;
+    __device__ __forceinline__ void start(const int32_t *lengths_, int first, int step_, int rows_, int T_) {
+        r = first; rows = rows_; step = step_; T = T_; lengths = lengths_;
+        t = b = dt = db = 0;
+        len = 1;
         if (lengths) {
-            if (rows + step < (int64_t(1) << 31)) {
-                const uint32_t T32 = static_cast<uint32_t>(T), f = static_cast<uint32_t>(first), s = static_cast<uint32_t>(step);
-                b = f / T32;
-                db = s / T32;
-            } else {
-                b = first / T;
-                db = step / T;
-            }
+            b = static_cast<int>(static_cast<uint32_t>(first) / static_cast<uint32_t>(T));
             t = first - b * T;
+            db = static_cast<int>(static_cast<uint32_t>(step) / static_cast<uint32_t>(T));
             dt = step - db * T;
+            if (in()) len = __ldg(lengths + b);
         }
     }
     __device__ __forceinline__ bool in() const { return r < rows; }
-    __device__ __forceinline__ bool valid() const { return lengths == nullptr || t < clamp_len(lengths, b, T); }
+    __device__ __forceinline__ bool valid() const { return t < len; }  // t in [0, T): lengths need no clamp
     __device__ __forceinline__ void next() {
         r += step;
         if (lengths) {
@@ -146,11 +167,12 @@ struct RowWalk {
                 t -= T;
                 ++b;
             }
+            if (in()) len = __ldg(lengths + b);
         }
     }
 };
 
-// Which of an octet's elements the dropout keeps: x[i] = 0 where not.
+// Which of an octet's elements the dropout keeps: zeros where not, whatever was there.
 struct Dropper {
     DropoutRng R;
     uint32_t thr16;  // threshold in the upper half of a word
@@ -160,13 +182,13 @@ struct Dropper {
         all = thr >= 65536u;
         thr16 = thr << 16;
     }
-    __device__ __forceinline__ void apply(uint64_t g, float (&x)[8]) const {
+    __device__ __forceinline__ void apply(uint64_t g, float2 (&x)[4]) const {
         const uint4 w4 = R.block(g);
         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (all || (w[i] << 16) < thr16) x[2 * i] = 0.f;
-            if (all || w[i] < thr16) x[2 * i + 1] = 0.f;
+            if (all || (w[i] << 16) < thr16) x[i].x = 0.f;
+            if (all || w[i] < thr16) x[i].y = 0.f;
         }
     }
 };
@@ -174,49 +196,35 @@ struct Dropper {
 // Sum over the TPR threads of a row (8, 16 or 32 lanes of a warp, or a whole block of TPR), the
 // same in all of them.  Blocks: `red` holds 2 x TPR/32 values; `flip` alternates its halves, so
 // one barrier per sum is enough.
-template <int TPR>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2 *red, int &flip) {
-    constexpr int W = TPR > 32 ? 32 : TPR;
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    if constexpr (TPR > 32) {
-        float2 *half = red + flip * (TPR / 32);
-        flip ^= 1;
-        if (threadIdx.x % 32 == 0) half[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = half[0];
-#pragma unroll
-        for (int w = 1; w < TPR / 32; ++w) {
-            const float2 q = half[w];
-            v.x += q.x;
-            v.y += q.y;
-        }
-    }
-    return v;
+__device__ __forceinline__ float2 plus(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 shfl_xor(float2 v, int o) {
+    return make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
 }
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *red, int &flip) {
+__device__ __forceinline__ float shfl_xor(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+template <int TPR, typename V>
+__device__ __forceinline__ V row_sum(V v, V *red, int &flip) {
     constexpr int W = TPR > 32 ? 32 : TPR;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = W / 2; o > 0; o >>= 1) v = plus(v, shfl_xor(v, o));
     if constexpr (TPR > 32) {
-        float *half = red + flip * (TPR / 32);
+        V *half = red + flip * (TPR / 32);
         flip ^= 1;
         if (threadIdx.x % 32 == 0) half[threadIdx.x / 32] = v;
         __syncthreads();
         v = half[0];
 #pragma unroll
-        for (int w = 1; w < TPR / 32; ++w) v += half[w];
+        for (int w = 1; w < TPR / 32; ++w) v = plus(v, half[w]);
     }
     return v;
 }
 
-// Position of channel c in shared memory when a lane reads 8 consecutive channels one by one (the
-// SHIFT kernels): one word of padding per 32 puts the 32 lanes' words in 32 banks.
-__device__ __forceinline__ int pad32(int c) { return c + (c >> 5); }
+// 1 / sqrt(v): the approximate reciprocal square root and one Newton step, under 2 units of 2^-24.
+// (0 and infinity keep the approximation's infinity and 0.)
+__device__ __forceinline__ float rsqrt_newton(float v) {
+    const float r = rsqrtf(v), e = fmaf(-v * r, r, 1.f);
+    return v > 0.f && v < INFINITY ? fmaf(0.5f * r, e, r) : r;
+}
 
 // Sums of two values over a block of W warps, the same in every thread.  `red` holds 2 * W floats;
 // the caller alternates two of them between calls, so one barrier per call is enough.
