@@ -8,11 +8,13 @@
 namespace dwk {
 namespace lnb {
 
+enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual add; with dropout too
+
 // TPR threads hold a row's NO octets each in registers.  Every thread keeps its channels from row to
 // row, so dgamma and dbeta add up in registers over all its rows; the block's groups are then added
 // in a fixed order through shared memory into the block's partial row.  SHIFT: rows that do not
 // start on an octet (C not a multiple of 8).
-template <typename T, int TPR, int NO, int THREADS, bool SHIFT, bool DROP>
+template <typename T, int TPR, int NO, int THREADS, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(THREADS)
 layernorm_bwd_rows_kernel(const ResidualArgs a) {
     constexpr int GPB = THREADS / TPR, W = THREADS / 32, HALF = W / 2;
@@ -20,8 +22,8 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
     extern __shared__ float sp[];  // SHIFT: gamma; at the end the warps' dgamma, dbeta
     launch_dependents();
     const int g = threadIdx.x / TPR, grid = gridDim.x, rows = static_cast<int>(a.B * a.T);
-    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy), *dh = static_cast<const T *>(a.dh);
-    T *dx = static_cast<T *>(a.dx), *dres = static_cast<T *>(a.dres);
+    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy), *dh = MODE == kPlain ? nullptr : static_cast<const T *>(a.dh);
+    T *dx = static_cast<T *>(a.dx), *dres = MODE == kPlain ? nullptr : static_cast<T *>(a.dres);
     Channels<T, TPR, NO, SHIFT> ch;
     ch.lane = threadIdx.x % TPR;
     ch.C = static_cast<int>(a.C);
@@ -40,7 +42,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
         __syncthreads();
     }
     Dropper D;
-    if constexpr (DROP) D.start(a.rng, a.thr);
+    if constexpr (MODE == kFusedDrop) D.start(a.rng, a.thr);
     const float inv = 1.f / static_cast<float>(ch.C);
     int flip = 0;
     float2 ag[NO][4] = {}, ab[NO][4] = {};
@@ -59,13 +61,24 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            xo[j].zero();
-            go[j].zero();
+            if (!(TPR >= 32 && j < NO - 1)) {
+                xo[j].zero();
+                go[j].zero();
+            }
             ho[j].zero();
-            if (!live || !ch.any(j)) continue;
-            ch.load(x, e, j, xo[j]);
-            ch.load(dy, e, j, go[j]);
-            if (dh) ch.load(dh, e, j, ho[j]);
+        }
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+                if (ch.any(j)) ch.load(x, e, j, xo[j]);
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+                if (ch.any(j)) ch.load(dy, e, j, go[j]);
+            if (MODE != kPlain && dh) {
+#pragma unroll
+                for (int j = 0; j < NO; ++j)
+                    if (ch.any(j)) ch.load(dh, e, j, ho[j]);
+            }
         }
         if (in && !live) {
             const float2 zero[4] = {};
@@ -81,7 +94,6 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
         float2 gg[NO][4];
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            if (!ch.any(j)) continue;
             float2 f[4], ga[4];
             xo[j].get(f);
             go[j].get(gg[j]);
@@ -89,9 +101,11 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
                 ch.clear_outside(j, f);
                 ch.clear_outside(j, gg[j]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ga[i] = make_float2(sp[off[2 * i] + j * TPR], sp[off[2 * i + 1] + j * TPR]);
+                for (int i = 0; i < 4; ++i)
+                    ga[i] = ch.any(j) ? make_float2(sp[off[2 * i] + j * TPR], sp[off[2 * i + 1] + j * TPR]) : make_float2(0.f, 0.f);
             } else {
-                load_params8(a.gamma ? a.gamma + ch.c0(j) : nullptr, 1.f, ga);
+                // behind the row: any channel's gamma will do, dy is zero there
+                load_params8(a.gamma + (ch.any(j) ? ch.c0(j) : 0), ga);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -118,9 +132,10 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
                 f[i] = ffma2(both(rstd), fadd2(gg[j][i], ffma2(xh, both(-c2), both(-c1))), d[i]);
             }
             if (dres) ch.store(dres, e, j, f);
-            if constexpr (DROP) D.apply(static_cast<uint64_t>(e + 8 * j * TPR) >> 3, f);
+            if constexpr (MODE == kFusedDrop) D.apply(static_cast<uint64_t>(e + 8 * j * TPR) >> 3, f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = fmul2(f[i], both(a.mult));
+            for (int i = 0; i < 4; ++i)
+                if (MODE != kPlain) f[i] = fmul2(f[i], both(a.mult));
             ch.store(dx, e, j, f);
         }
     }
@@ -175,10 +190,10 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
     }
 }
 
-template <typename T, int TPR, int NO, int THREADS, bool SHIFT, bool DROP>
+template <typename T, int TPR, int NO, int THREADS, bool SHIFT, int MODE>
 cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     constexpr int GPB = THREADS / TPR, HALF = THREADS / 64;
-    const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, THREADS, SHIFT, DROP>;
+    const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, THREADS, SHIFT, MODE>;
     const size_t words = 8 * static_cast<size_t>((a.C + 7) / 8 + 2);
     size_t smem = SHIFT ? words * sizeof(float) : 0;
     if (TPR <= 32) smem = HALF * 2 * words * sizeof(float);
@@ -207,7 +222,9 @@ template <typename T> constexpr int threads_for(int NO) {
 template <typename T, int TPR, int NO, bool SHIFT>
 cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     constexpr int kThreads = TPR > 32 ? TPR : threads_for<T>(NO);
-    return a.thr ? launch<T, TPR, NO, kThreads, SHIFT, true>(a, G, s) : launch<T, TPR, NO, kThreads, SHIFT, false>(a, G, s);
+    if (a.thr) return launch<T, TPR, NO, kThreads, SHIFT, kFusedDrop>(a, G, s);
+    if (a.dh || a.dres || a.mult != 1.f) return launch<T, TPR, NO, kThreads, SHIFT, kFused>(a, G, s);
+    return launch<T, TPR, NO, kThreads, SHIFT, kPlain>(a, G, s);
 }
 
 template <typename T, bool SHIFT>
@@ -221,6 +238,7 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, int *G, cudaStream_t
     if (n <= 160) return launch<T, 32, 5, SHIFT>(a, G, s);
     if (n <= 256) return launch<T, 256, 1, SHIFT>(a, G, s);
     if (n <= 512) return launch<T, 256, 2, SHIFT>(a, G, s);
+    if (n <= 768) return launch<T, 384, 2, SHIFT>(a, G, s);
     if (n <= 1024) return launch<T, 512, 2, SHIFT>(a, G, s);
     return cudaErrorNotSupported;
 }
@@ -228,8 +246,8 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, int *G, cudaStream_t
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, int *G, cudaStream_t s) {
-    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30)) return cudaErrorNotSupported;
-    if (a.C % 8 == 0 && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0) return launch_octets<T, false>(a, a.C / 8, G, s);
+    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u) return cudaErrorNotSupported;
+    if (a.C % 8 == 0 && a.gamma && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0) return launch_octets<T, false>(a, a.C / 8, G, s);
     return launch_octets<T, true>(a, (a.C + 14) / 8, G, s);  // a row may touch 7 elements before its first
 }
 

@@ -10,10 +10,13 @@ namespace lnf {
 
 constexpr int threads_for(int TPR) { return TPR > 256 ? TPR : 256; }
 
+enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual add; with dropout too
+
 // TPR threads hold a row's NO octets each in registers: one read of x (and res), the mean, then
 // the variance of the centred values, then the outputs; the next row's octets are requested first.
-// SHIFT: rows that do not start on an octet (C not a multiple of 8).
-template <typename T, int TPR, int NO, bool SHIFT, bool DROP>
+// SHIFT: rows that do not start on an octet (C not a multiple of 8), or a parameter missing or
+// misaligned; gamma and beta then come from shared memory instead of L1.
+template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(threads_for(TPR))
 layernorm_fwd_rows_kernel(const ResidualArgs a) {
     constexpr int kThreads = threads_for(TPR), GPB = kThreads / TPR;
@@ -21,8 +24,8 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     extern __shared__ float2 sp[];  // SHIFT: {gamma, beta} per channel
     launch_dependents();
     const int g = threadIdx.x / TPR, grid = gridDim.x, rows = static_cast<int>(a.B * a.T);
-    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
-    T *y = static_cast<T *>(a.y), *h = static_cast<T *>(a.h);
+    const T *x = static_cast<const T *>(a.x), *res = MODE == kPlain ? nullptr : static_cast<const T *>(a.res);
+    T *y = static_cast<T *>(a.y), *h = MODE == kPlain ? nullptr : static_cast<T *>(a.h);
     Channels<T, TPR, NO, SHIFT> ch;
     ch.lane = threadIdx.x % TPR;
     ch.C = static_cast<int>(a.C);
@@ -43,7 +46,7 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         __syncthreads();
     }
     Dropper D;
-    if constexpr (DROP) D.start(a.rng, a.thr);
+    if constexpr (MODE == kFusedDrop) D.start(a.rng, a.thr);
     const float inv = 1.f / static_cast<float>(ch.C);
     int flip = 0;
     Oct<T> xo[NO], ro[NO];
@@ -51,10 +54,12 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         if (!w.in() || !w.valid()) return;
         const int64_t e = ch.at(w.r);
 #pragma unroll
-        for (int j = 0; j < NO; ++j) {
-            if (!ch.any(j)) continue;
-            ch.load(x, e, j, xo[j]);
-            if (res) ch.load(res, e, j, ro[j]);
+        for (int j = 0; j < NO; ++j)
+            if (ch.any(j)) ch.load(x, e, j, xo[j]);
+        if (MODE != kPlain && res) {
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+                if (ch.any(j)) ch.load(res, e, j, ro[j]);
         }
     };
 #pragma unroll
@@ -74,12 +79,14 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         float2 v[NO][4], sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            float2 p[4];
             xo[j].get(v[j]);
-            ro[j].get(p);
-            if constexpr (DROP) D.apply(static_cast<uint64_t>(e + 8 * j * TPR) >> 3, v[j]);
+            if constexpr (MODE == kFusedDrop) D.apply(static_cast<uint64_t>(e + 8 * j * TPR) >> 3, v[j]);
+            if constexpr (MODE != kPlain) {
+                float2 p[4];
+                ro[j].get(p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[j][i] = ffma2(both(a.mult), v[j][i], p[i]);
+                for (int i = 0; i < 4; ++i) v[j][i] = ffma2(both(a.mult), v[j][i], p[i]);
+            }
             if constexpr (SHIFT) ch.clear_outside(j, v[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum = fadd2(sum, v[j][i]);
@@ -101,14 +108,17 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         }
         if (TPR >= 32 && !live) continue;
         const float mean = row_sum<TPR>(sum.x + sum.y, red, flip) * inv;
+        if (MODE != kPlain && h && live) {
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+                if (ch.any(j)) ch.store(h, e, j, v[j]);
+        }
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            if (!ch.any(j)) continue;
-            if (h && live) ch.store(h, e, j, v[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[j][i] = fadd2(v[j][i], both(-mean));
-            if constexpr (SHIFT) ch.clear_outside(j, v[j]);
+            ch.clear_outside(j, v[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) ss = ffma2(v[j][i], v[j][i], ss);
         }
@@ -126,8 +136,8 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
                         be[i] = make_float2(p.y, q.y);
                     }
                 } else {
-                    load_params8(a.gamma ? a.gamma + ch.c0(j) : nullptr, 1.f, ga);
-                    load_params8(a.beta ? a.beta + ch.c0(j) : nullptr, 0.f, be);
+                    load_params8(a.gamma + ch.c0(j), ga);
+                    load_params8(a.beta + ch.c0(j), be);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[j][i] = ffma2(fmul2(v[j][i], both(rstd)), ga[i], be[i]);
@@ -141,10 +151,10 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     }
 }
 
-template <typename T, int TPR, int NO, bool SHIFT, bool DROP>
+template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 cudaError_t launch(const ResidualArgs &a, cudaStream_t s) {
     constexpr int kThreads = threads_for(TPR), GPB = kThreads / TPR;
-    const auto kern = layernorm_fwd_rows_kernel<T, TPR, NO, SHIFT, DROP>;
+    const auto kern = layernorm_fwd_rows_kernel<T, TPR, NO, SHIFT, MODE>;
     const size_t smem = SHIFT ? 8 * ((a.C + 7) / 8 + 2) * sizeof(float2) : 0;
     static const int regs_per_sm = [&] {
         int n = 0;
@@ -165,7 +175,9 @@ cudaError_t launch(const ResidualArgs &a, cudaStream_t s) {
 
 template <typename T, int TPR, int NO, bool SHIFT>
 cudaError_t launch(const ResidualArgs &a, cudaStream_t s) {
-    return a.thr ? launch<T, TPR, NO, SHIFT, true>(a, s) : launch<T, TPR, NO, SHIFT, false>(a, s);
+    if (a.thr) return launch<T, TPR, NO, SHIFT, kFusedDrop>(a, s);
+    if (a.res || a.h || a.mult != 1.f) return launch<T, TPR, NO, SHIFT, kFused>(a, s);
+    return launch<T, TPR, NO, SHIFT, kPlain>(a, s);
 }
 
 template <typename T, bool SHIFT>
@@ -182,6 +194,7 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, cudaStream_t s) {
     if (n <= 160) return launch<T, 32, 5, SHIFT>(a, s);
     if (n <= 256) return launch<T, 256, 1, SHIFT>(a, s);
     if (n <= 512) return launch<T, 256, 2, SHIFT>(a, s);
+    if (n <= 768) return launch<T, 256, 3, SHIFT>(a, s);
     if (n <= 1024) return launch<T, 256, 4, SHIFT>(a, s);
     return cudaErrorNotSupported;
 }
@@ -189,8 +202,8 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, cudaStream_t s) {
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, cudaStream_t s) {
-    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30)) return cudaErrorNotSupported;
-    const bool params32 = reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0 && reinterpret_cast<uintptr_t>(a.beta) % 32 == 0;
+    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u) return cudaErrorNotSupported;
+    const bool params32 = a.gamma && a.beta && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0 && reinterpret_cast<uintptr_t>(a.beta) % 32 == 0;
     if (a.C % 8 == 0 && params32) return launch_octets<T, false>(a, a.C / 8, s);
     return launch_octets<T, true>(a, (a.C + 14) / 8, s);  // a row may touch 7 elements before its first
 }

@@ -66,12 +66,8 @@ template <> struct Oct<float> {
     }
 };
 
-// Eight float32 parameters (32-byte aligned), kept in L1 for the rows to come; `missing` without any.
-__device__ __forceinline__ void load_params8(const float *p, float missing, float2 (&f)[4]) {
-    if (p == nullptr) {
-        f[0] = f[1] = f[2] = f[3] = both(missing);
-        return;
-    }
+// Eight float32 parameters (32-byte aligned), kept in L1 for the rows to come.
+__device__ __forceinline__ void load_params8(const float *p, float2 (&f)[4]) {
     asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y), "=f"(f[2].x), "=f"(f[2].y), "=f"(f[3].x),
                    "=f"(f[3].y)
@@ -82,13 +78,17 @@ __device__ __forceinline__ void load_params8(const float *p, float missing, floa
 // Octets lie on multiples of 8 of the flat index, so every one is an aligned word whatever C is: a row
 // starts s = (r C) mod 8 elements into its first octet, and octet v holds its channels 8 v - s ..
 // 8 v - s + 7.  SHIFT false: C is a multiple of 8, s = 0.  A thread's rows are a multiple of 8
-// apart, so it keeps its s and its channels.
+// apart, so it keeps its s and its channels.  A row has more than TPR (NO - 1) octets (SHIFT: may touch
+// that many), so only the last octet of a thread can lie behind the row, and only the first one
+// and the last two can be partial.
 template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
     int lane, s, C;
     int64_t N;  // elements of the tensor
     __device__ __forceinline__ int c0(int j) const { return 8 * (j * TPR + lane) - s; }
-    __device__ __forceinline__ bool any(int j) const { return c0(j) < C; }
-    __device__ __forceinline__ bool full(int j) const { return !SHIFT || (c0(j) >= 0 && c0(j) + 8 <= C); }
+    __device__ __forceinline__ bool any(int j) const { return j < NO - 1 || c0(j) < C; }
+    __device__ __forceinline__ bool full(int j) const {
+        return !SHIFT || (j > 0 && j < NO - 2) || (c0(j) >= 0 && c0(j) + 8 <= C);
+    }
     __device__ __forceinline__ bool has(int j, int i) const {
         return !SHIFT || static_cast<unsigned>(c0(j) + i) < static_cast<unsigned>(C);
     }
@@ -122,8 +122,16 @@ template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
             }
         }
     }
-    // Zeros in the places of a partial octet that are not this row's.
+    // Zeros in the places of an octet that are not this row's.
     __device__ __forceinline__ void clear_outside(int j, float2 (&f)[4]) const {
+        if (!SHIFT) {
+            if (j == NO - 1) {
+                const bool in = any(j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = in ? f[i] : make_float2(0.f, 0.f);
+            }
+            return;
+        }
         if (full(j)) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -172,14 +180,12 @@ struct RowWalk {
     }
 };
 
-// Which of an octet's elements the dropout keeps: zeros where not, whatever was there.
+// Which of an octet's elements the dropout keeps: zeros where not, whatever was there.  thr < 65536.
 struct Dropper {
     DropoutRng R;
     uint32_t thr16;  // threshold in the upper half of a word
-    bool all;        // thr = 65536: nothing is kept
     __device__ __forceinline__ void start(const unsigned long long *rng, uint32_t thr) {
         R.load(rng);
-        all = thr >= 65536u;
         thr16 = thr << 16;
     }
     __device__ __forceinline__ void apply(uint64_t g, float2 (&x)[4]) const {
@@ -187,8 +193,8 @@ struct Dropper {
         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (all || (w[i] << 16) < thr16) x[i].x = 0.f;
-            if (all || w[i] < thr16) x[i].y = 0.f;
+            x[i].x = (w[i] << 16) < thr16 ? 0.f : x[i].x;
+            x[i].y = w[i] < thr16 ? 0.f : x[i].y;
         }
     }
 };
