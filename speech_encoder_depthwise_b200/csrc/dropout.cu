@@ -65,29 +65,44 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
     Dropper D;
     if constexpr (DROP) D.start(rng, thr);
     const int64_t mine = first + threadIdx.x * 8;
-    int st[U];
-    {
-        const int64_t start = b * TC, lim = lengths ? start + clamp_len(lengths, b, Tn) * C : N;
-        const bool whole = first + kChunk <= N;
-        if (whole && first + kChunk <= lim) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) st[u] = kValid;
-        } else if (whole && first >= lim && first + kChunk <= start + TC) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) st[u] = kMasked;
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t e = mine + u * kStep;
-                st[u] = kNone;
-                if (e >= N) continue;
-                const int64_t item = lengths ? item_of(e) : 0, i0 = lengths ? item * TC : 0;
-                const int64_t i1 = lengths ? i0 + clamp_len(lengths, item, Tn) * C : N, i2 = lengths ? i0 + TC : N;
-                st[u] = e + 8 <= i1 ? kValid : (e >= i1 && e + 8 <= i2 ? kMasked : kMixed);
-            }
-        }
-    }
+    const int64_t start = b * TC, lim = lengths ? start + clamp_len(lengths, b, Tn) * C : N;
     Oct<T> xo[U], ro[U];
+    if (first + kChunk <= lim) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) xo[u].load(x + mine + u * kStep);
+        if constexpr (RES) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) ro[u].load(res + mine + u * kStep);
+        }
+        float2 f[U][4], q[4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) xo[u].get(f[u]);
+        if constexpr (DROP) D.apply(static_cast<uint32_t>(mine >> 3), kStep / 8, f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (RES) ro[u].get(q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[u][i] = RES ? ffma2(both(mult), f[u][i], q[i]) : fmul2(both(mult), f[u][i]);
+            Oct<T>::store(y + mine + u * kStep, f[u]);
+        }
+        return;
+    }
+    if (first >= lim && first + kChunk <= start + TC && first + kChunk <= N) {
+        const float2 zero[4] = {};
+#pragma unroll
+        for (int u = 0; u < U; ++u) Oct<T>::store(y + mine + u * kStep, zero);
+        return;
+    }
+    int st[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t e = mine + u * kStep;
+        st[u] = kNone;
+        if (e >= N) continue;
+        const int64_t item = lengths ? item_of(e) : 0, i0 = lengths ? item * TC : 0;
+        const int64_t i1 = lengths ? i0 + clamp_len(lengths, item, Tn) * C : N, i2 = lengths ? i0 + TC : N;
+        st[u] = e + 8 <= i1 ? kValid : (e >= i1 && e + 8 <= i2 ? kMasked : kMixed);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (st[u] != kValid) continue;
@@ -96,15 +111,15 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float2 f[4] = {}, q[4] = {};
+        float2 f[1][4] = {}, q[4] = {};
         if (st[u] == kValid) {
-            xo[u].get(f);
+            xo[u].get(f[0]);
             if constexpr (RES) ro[u].get(q);
-            if constexpr (DROP) D.apply(static_cast<uint64_t>(mine + u * kStep) >> 3, f);
+            if constexpr (DROP) D.apply(static_cast<uint32_t>((mine + u * kStep) >> 3), 0, f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = RES ? ffma2(both(mult), f[i], q[i]) : fmul2(both(mult), f[i]);
+            for (int i = 0; i < 4; ++i) f[0][i] = RES ? ffma2(both(mult), f[0][i], q[i]) : fmul2(both(mult), f[0][i]);
         }
-        if (st[u] <= kMasked) Oct<T>::store(y + mine + u * kStep, f);
+        if (st[u] <= kMasked) Oct<T>::store(y + mine + u * kStep, f[0]);
     }
     unsigned mixed = 0;
 #pragma unroll
@@ -113,8 +128,8 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
     for (int u = 0; mixed; ++u, mixed >>= 1) {
         if (!(mixed & 1u)) continue;
         const int64_t e0 = mine + u * kStep;
-        float2 keep[4] = {both(1.f), both(1.f), both(1.f), both(1.f)};
-        if constexpr (DROP) D.apply(static_cast<uint64_t>(e0) >> 3, keep);
+        float2 keep[1][4] = {{both(1.f), both(1.f), both(1.f), both(1.f)}};
+        if constexpr (DROP) D.apply(static_cast<uint32_t>(e0 >> 3), 0, keep);
         int64_t item = lengths ? item_of(e0) : 0, next = lengths ? (item + 1) * TC : N;
         int64_t lim = lengths ? item * TC + clamp_len(lengths, item, Tn) * C : N;
 #pragma unroll
@@ -128,7 +143,7 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
             float v = 0.f;
             if (e < lim) {
                 if constexpr (RES) v = load1(res + e);
-                if ((i % 2 ? keep[i / 2].y : keep[i / 2].x) != 0.f) v = fmaf(mult, load1(x + e), v);
+                if ((i % 2 ? keep[0][i / 2].y : keep[0][i / 2].x) != 0.f) v = fmaf(mult, load1(x + e), v);
             }
             store1(y + e, v);
         }
@@ -150,7 +165,7 @@ cudaError_t launch_octets(const ResidualArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t dropout_add_launch(const ResidualArgs &a, cudaStream_t s) {
-    if (a.vec_oct && a.thr < 65536) return with_dtype(a.dtype, [&](auto t) { return launch_octets<decltype(t)>(a, s); });
+    if (a.vec_oct && a.thr < 65536 && a.B * a.T * a.C < (int64_t(1) << 35)) return with_dtype(a.dtype, [&](auto t) { return launch_octets<decltype(t)>(a, s); });
     const int64_t groups = (a.B * a.T * a.C + 7) / 8;
     const int64_t blocks = (groups + 255) / 256, most = static_cast<int64_t>(sm_count()) * 8;
     const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));

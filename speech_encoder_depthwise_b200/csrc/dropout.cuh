@@ -23,22 +23,32 @@ struct DropoutRng {
         o1 = static_cast<uint32_t>(offset >> 32);
     }
 
-    // The block of elements 8 g .. 8 g + 7: element 8 g + i in bits 16 (i % 2) .. of word i / 2.
-    __device__ __forceinline__ uint4 block(uint64_t g) const {
-        uint32_t c0 = static_cast<uint32_t>(g), c1 = static_cast<uint32_t>(g >> 32), c2 = o0, c3 = o1;
+    // The blocks g + j step, j < NO: block g has elements 8 g .. 8 g + 7, element 8 g + i in bits
+    // 16 (i % 2) .. of word i / 2.
+    template <int NO, typename G> __device__ __forceinline__ void blocks(G g, uint32_t step, uint4 (&w)[NO]) const {
         uint32_t a = k0, b = k1;
 #pragma unroll
+        for (int j = 0; j < NO; ++j) {
+            const uint64_t gj = static_cast<G>(g + static_cast<G>(j) * step);
+            w[j] = make_uint4(static_cast<uint32_t>(gj), static_cast<uint32_t>(gj >> 32), o0, o1);
+        }
+#pragma unroll
         for (int r = 0; r < 10; ++r) {
-            const uint64_t p = static_cast<uint64_t>(c0) * 0xD2511F53u, q = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-            const uint32_t n0 = static_cast<uint32_t>(q >> 32) ^ c1 ^ a, n2 = static_cast<uint32_t>(p >> 32) ^ c3 ^ b;
-            c1 = static_cast<uint32_t>(q);
-            c3 = static_cast<uint32_t>(p);
-            c0 = n0;
-            c2 = n2;
+#pragma unroll
+            for (int j = 0; j < NO; ++j) {
+                const uint64_t p = static_cast<uint64_t>(w[j].x) * 0xD2511F53u, q = static_cast<uint64_t>(w[j].z) * 0xCD9E8D57u;
+                w[j] = make_uint4(static_cast<uint32_t>(q >> 32) ^ w[j].y ^ a, static_cast<uint32_t>(q),
+                                  static_cast<uint32_t>(p >> 32) ^ w[j].w ^ b, static_cast<uint32_t>(p));
+            }
             a += 0x9E3779B9u;
             b += 0xBB67AE85u;
         }
-        return make_uint4(c0, c1, c2, c3);
+    }
+
+    __device__ __forceinline__ uint4 block(uint64_t g) const {
+        uint4 w[1];
+        blocks<1>(g, 0, w);
+        return w[0];
     }
 
     // Whether one element is kept (a whole block per call: the slow, general form).

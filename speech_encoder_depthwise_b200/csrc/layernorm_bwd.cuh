@@ -24,12 +24,12 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
     const int g = threadIdx.x / TPR, grid = gridDim.x, rows = static_cast<int>(a.B * a.T);
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy), *dh = MODE == kPlain ? nullptr : static_cast<const T *>(a.dh);
     T *dx = static_cast<T *>(a.dx), *dres = MODE == kPlain ? nullptr : static_cast<T *>(a.dres);
-    Channels<T, TPR, NO, SHIFT> ch;
-    ch.lane = threadIdx.x % TPR;
-    ch.C = static_cast<int>(a.C);
-    ch.N = rows * a.C;
-    const int first = blockIdx.x + grid * g, Q = shifted_q(ch.C);
-    ch.s = SHIFT ? static_cast<int>((first * a.C) % 8) : 0;
+    using Ch = Channels<T, TPR, NO, SHIFT>;
+    __shared__ __align__(32) T scratch[SHIFT ? THREADS / Ch::kGroup * 16 : 1];
+    Ch ch;
+    const int first = blockIdx.x + grid * g;
+    ch.start(static_cast<int>(a.C), rows, first, scratch);
+    const int Q = shifted_q(ch.C);
     int off[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) off[i] = shifted_off(i, ch.s, Q) + ch.lane;
@@ -68,38 +68,23 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
             ho[j].zero();
         }
         if (live) {
-#pragma unroll
-            for (int j = 0; j < NO; ++j)
-                if (ch.any(j)) ch.load(x, e, j, xo[j]);
-#pragma unroll
-            for (int j = 0; j < NO; ++j)
-                if (ch.any(j)) ch.load(dy, e, j, go[j]);
-            if (MODE != kPlain && dh) {
-#pragma unroll
-                for (int j = 0; j < NO; ++j)
-                    if (ch.any(j)) ch.load(dh, e, j, ho[j]);
-            }
+            ch.load_row(x, e, w.r, xo);
+            ch.load_row(dy, e, w.r, go);
+            if (MODE != kPlain && dh) ch.load_row(dh, e, w.r, ho);
         }
         if (in && !live) {
-            const float2 zero[4] = {};
-#pragma unroll
-            for (int j = 0; j < NO; ++j) {
-                if (!ch.any(j)) continue;
-                ch.store(dx, e, j, zero);
-                if (dres) ch.store(dres, e, j, zero);
-            }
+            ch.store_zeros(dx, e, true);
+            if (dres) ch.store_zeros(dres, e, true);
         }
         if (TPR >= 32 && !live) continue;
         float2 s1 = make_float2(0.f, 0.f), s2 = s1;
-        float2 gg[NO][4];
+        float2 gg[NO][4], xh[NO][4];
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            float2 f[4], ga[4];
-            xo[j].get(f);
-            go[j].get(gg[j]);
+            float2 ga[4];
+            ch.get(j, xo[j], xh[j]);
+            ch.get(j, go[j], gg[j]);
             if constexpr (SHIFT) {
-                ch.clear_outside(j, f);
-                ch.clear_outside(j, gg[j]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     ga[i] = ch.any(j) ? make_float2(sp[off[2 * i] + j * TPR], sp[off[2 * i + 1] + j * TPR]) : make_float2(0.f, 0.f);
@@ -109,35 +94,35 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 xh = fmul2(fadd2(f[i], both(-mean)), both(rstd));
-                ag[j][i] = ffma2(gg[j][i], xh, ag[j][i]);
+                xh[j][i] = fmul2(fadd2(xh[j][i], both(-mean)), both(rstd));
+                ag[j][i] = ffma2(gg[j][i], xh[j][i], ag[j][i]);
                 ab[j][i] = fadd2(ab[j][i], gg[j][i]);
                 gg[j][i] = fmul2(gg[j][i], ga[i]);
                 s1 = fadd2(s1, gg[j][i]);
-                s2 = ffma2(gg[j][i], xh, s2);
+                s2 = ffma2(gg[j][i], xh[j][i], s2);
             }
         }
         const float2 sum = row_sum<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red, flip);
         const float c1 = sum.x * inv, c2 = sum.y * inv;
-        if (!live) continue;
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            if (!ch.any(j)) continue;
-            float2 f[4], d[4];
-            xo[j].get(f);
-            ho[j].get(d);
+            float2 d[4] = {};
+            if constexpr (MODE != kPlain) ho[j].get(d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 xh = fmul2(fadd2(f[i], both(-mean)), both(rstd));
-                f[i] = ffma2(both(rstd), fadd2(gg[j][i], ffma2(xh, both(-c2), both(-c1))), d[i]);
+                const float2 t = fadd2(gg[j][i], ffma2(xh[j][i], both(-c2), both(-c1)));
+                gg[j][i] = MODE == kPlain ? fmul2(both(rstd), t) : ffma2(both(rstd), t, d[i]);
             }
-            if (dres) ch.store(dres, e, j, f);
-            if constexpr (MODE == kFusedDrop) D.apply(static_cast<uint64_t>(e + 8 * j * TPR) >> 3, f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (MODE != kPlain) f[i] = fmul2(f[i], both(a.mult));
-            ch.store(dx, e, j, f);
         }
+        if (MODE != kPlain && dres) ch.store_row(dres, e, live, gg);
+        if constexpr (MODE != kPlain) {
+            if constexpr (MODE == kFusedDrop) D.apply(static_cast<uint32_t>(e >> 3), TPR, gg);
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gg[j][i] = fmul2(gg[j][i], both(a.mult));
+        }
+        ch.store_row(dx, e, live, gg);
     }
     if (!a.dgamma && !a.dbeta) return;
     // a warp's or block's sums by channel, in the shifted layout: dgamma at slot[at], dbeta at slot[8 Q + at]
@@ -215,8 +200,8 @@ cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
 // Threads of a block (one or two blocks on an SM): as many as the registers of NO octets leave room
 // for, a multiple of 64.
 template <typename T> constexpr int threads_for(int NO) {
-    return sizeof(T) == 2 ? (NO == 1 ? 1024 : NO == 2 ? 640 : NO == 3 ? 512 : NO == 4 ? 384 : 320)
-                          : (NO == 1 ? 768 : NO == 2 ? 512 : NO == 3 ? 384 : NO == 4 ? 320 : 256);
+    return sizeof(T) == 2 ? (NO == 1 ? 1024 : NO == 2 ? 640 : NO == 3 ? 512 : NO == 4 ? 384 : 256)
+                          : (NO == 1 ? 768 : NO == 2 ? 512 : NO == 3 ? 384 : 256);
 }
 
 template <typename T, int TPR, int NO, bool SHIFT>
@@ -246,7 +231,8 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, int *G, cudaStream_t
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, int *G, cudaStream_t s) {
-    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u) return cudaErrorNotSupported;
+    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u ||
+        a.B * a.T * a.C >= (int64_t(1) << 35)) return cudaErrorNotSupported;
     if (a.C % 8 == 0 && a.gamma && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0) return launch_octets<T, false>(a, a.C / 8, G, s);
     return launch_octets<T, true>(a, (a.C + 14) / 8, G, s);  // a row may touch 7 elements before its first
 }

@@ -17,7 +17,7 @@ enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual ad
 // SHIFT: rows that do not start on an octet (C not a multiple of 8), or a parameter missing or
 // misaligned; gamma and beta then come from shared memory instead of L1.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
-__global__ void __launch_bounds__(threads_for(TPR))
+__global__ void __launch_bounds__(threads_for(TPR), 2)
 layernorm_fwd_rows_kernel(const ResidualArgs a) {
     constexpr int kThreads = threads_for(TPR), GPB = kThreads / TPR;
     __shared__ float red[2 * (TPR > 32 ? TPR / 32 : 1)];
@@ -26,12 +26,11 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     const int g = threadIdx.x / TPR, grid = gridDim.x, rows = static_cast<int>(a.B * a.T);
     const T *x = static_cast<const T *>(a.x), *res = MODE == kPlain ? nullptr : static_cast<const T *>(a.res);
     T *y = static_cast<T *>(a.y), *h = MODE == kPlain ? nullptr : static_cast<T *>(a.h);
-    Channels<T, TPR, NO, SHIFT> ch;
-    ch.lane = threadIdx.x % TPR;
-    ch.C = static_cast<int>(a.C);
-    ch.N = rows * a.C;
+    using Ch = Channels<T, TPR, NO, SHIFT>;
+    __shared__ __align__(32) T scratch[SHIFT ? kThreads / Ch::kGroup * 16 : 1];
+    Ch ch;
     const int first = blockIdx.x + grid * g;
-    ch.s = SHIFT ? static_cast<int>((first * a.C) % 8) : 0;
+    ch.start(static_cast<int>(a.C), rows, first, scratch);
     int off[8];
     grid_dependency_wait();
     if constexpr (SHIFT) {
@@ -53,54 +52,49 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     const auto fetch = [&](const RowWalk &w) {
         if (!w.in() || !w.valid()) return;
         const int64_t e = ch.at(w.r);
-#pragma unroll
-        for (int j = 0; j < NO; ++j)
-            if (ch.any(j)) ch.load(x, e, j, xo[j]);
-        if (MODE != kPlain && res) {
-#pragma unroll
-            for (int j = 0; j < NO; ++j)
-                if (ch.any(j)) ch.load(res, e, j, ro[j]);
-        }
+        ch.load_row(x, e, w.r, xo);
+        if (MODE != kPlain && res) ch.load_row(res, e, w.r, ro);
     };
 #pragma unroll
     for (int j = 0; j < NO; ++j) {
         xo[j].zero();
         ro[j].zero();
     }
+    // the next row is requested ahead where two rows fit 128 registers a thread
+    constexpr bool kAhead = NO * sizeof(T) * (MODE == kPlain ? 1 : 2) <= 16;
     RowWalk w;
     w.start(a.lengths, first, grid * GPB, rows, static_cast<int>(a.T));
-    fetch(w);
+    if (kAhead) fetch(w);
     // groups of one warp walk together (their sums share its shuffles): until the first one is done
     int lead = TPR < 32 ? blockIdx.x + grid * (threadIdx.x / 32 * (32 / TPR)) : first;
     for (; lead < rows; lead += w.step) {
+        if (!kAhead) fetch(w);
         const bool in = w.in(), live = in && w.valid();
         const int r = w.r;
         const int64_t e = ch.at(r);
         float2 v[NO][4], sum = make_float2(0.f, 0.f);
+        if constexpr (MODE == kFusedDrop) {
+#pragma unroll
+            for (int j = 0; j < NO; ++j) ch.get(j, xo[j], v[j]);
+            D.apply(static_cast<uint32_t>(e >> 3), TPR, v);
+        }
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            xo[j].get(v[j]);
-            if constexpr (MODE == kFusedDrop) D.apply(static_cast<uint64_t>(e + 8 * j * TPR) >> 3, v[j]);
+            if constexpr (MODE != kFusedDrop) ch.get(j, xo[j], v[j]);
             if constexpr (MODE != kPlain) {
                 float2 p[4];
-                ro[j].get(p);
+                ch.get(j, ro[j], p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[j][i] = ffma2(both(a.mult), v[j][i], p[i]);
             }
-            if constexpr (SHIFT) ch.clear_outside(j, v[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum = fadd2(sum, v[j][i]);
         }
         w.next();
-        fetch(w);
+        if (kAhead) fetch(w);
         if (in && !live) {
-            const float2 zero[4] = {};
-#pragma unroll
-            for (int j = 0; j < NO; ++j) {
-                if (!ch.any(j)) continue;
-                ch.store(y, e, j, zero);
-                if (h) ch.store(h, e, j, zero);
-            }
+            ch.store_zeros(y, e, true);
+            if (h) ch.store_zeros(h, e, true);
             if (ch.lane == 0) {
                 if (a.mean) a.mean[r] = 0.f;
                 if (a.rstd) a.rstd[r] = 0.f;
@@ -108,11 +102,7 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         }
         if (TPR >= 32 && !live) continue;
         const float mean = row_sum<TPR>(sum.x + sum.y, red, flip) * inv;
-        if (MODE != kPlain && h && live) {
-#pragma unroll
-            for (int j = 0; j < NO; ++j)
-                if (ch.any(j)) ch.store(h, e, j, v[j]);
-        }
+        if (MODE != kPlain && h) ch.store_row(h, e, live, v);
         float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
@@ -123,30 +113,28 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
             for (int i = 0; i < 4; ++i) ss = ffma2(v[j][i], v[j][i], ss);
         }
         const float rstd = rsqrt_newton(fmaf(row_sum<TPR>(ss.x + ss.y, red, flip), inv, a.eps));
-        if (live) {
 #pragma unroll
-            for (int j = 0; j < NO; ++j) {
-                if (!ch.any(j)) continue;
-                float2 ga[4], be[4];
-                if constexpr (SHIFT) {
+        for (int j = 0; j < NO; ++j) {
+            const bool any = ch.any(j);  // behind the row: any channel's parameters will do
+            if constexpr (SHIFT) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 p = sp[off[2 * i] + j * TPR], q = sp[off[2 * i + 1] + j * TPR];
-                        ga[i] = make_float2(p.x, q.x);
-                        be[i] = make_float2(p.y, q.y);
-                    }
-                } else {
-                    load_params8(a.gamma + ch.c0(j), ga);
-                    load_params8(a.beta + ch.c0(j), be);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 p = sp[any ? off[2 * i] + j * TPR : 0], q = sp[any ? off[2 * i + 1] + j * TPR : 0];
+                    const float2 t = fmul2(v[j][i], both(rstd));
+                    v[j][i] = make_float2(fmaf(t.x, p.x, p.y), fmaf(t.y, q.x, q.y));
                 }
+            } else {
+                float2 ga[4], be[4];
+                load_params8(a.gamma + (any ? ch.c0(j) : 0), ga);
+                load_params8(a.beta + (any ? ch.c0(j) : 0), be);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[j][i] = ffma2(fmul2(v[j][i], both(rstd)), ga[i], be[i]);
-                ch.store(y, e, j, v[j]);
             }
-            if (ch.lane == 0) {
-                if (a.mean) a.mean[r] = mean;
-                if (a.rstd) a.rstd[r] = rstd;
-            }
+        }
+        ch.store_row(y, e, live, v);
+        if (ch.lane == 0 && live) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
         }
     }
 }
@@ -202,7 +190,8 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, cudaStream_t s) {
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, cudaStream_t s) {
-    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u) return cudaErrorNotSupported;
+    if (!a.vec_oct || a.C > 8192 || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u ||
+        a.B * a.T * a.C >= (int64_t(1) << 35)) return cudaErrorNotSupported;
     const bool params32 = a.gamma && a.beta && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0 && reinterpret_cast<uintptr_t>(a.beta) % 32 == 0;
     if (a.C % 8 == 0 && params32) return launch_octets<T, false>(a, a.C / 8, s);
     return launch_octets<T, true>(a, (a.C + 14) / 8, s);  // a row may touch 7 elements before its first
