@@ -23,13 +23,13 @@ struct DropoutRng {
         o1 = static_cast<uint32_t>(offset >> 32);
     }
 
-    // The blocks g + j step, j < NO: block g has elements 8 g .. 8 g + 7, element 8 g + i in bits
+    // The blocks g[0 .. NO-1]: block g has elements 8 g .. 8 g + 7, element 8 g + i in bits
     // 16 (i % 2) .. of word i / 2.
-    template <int NO, typename G> __device__ __forceinline__ void blocks(G g, uint32_t step, uint4 (&w)[NO]) const {
+    template <int NO, typename G> __device__ __forceinline__ void blocks(const G (&g)[NO], uint4 (&w)[NO]) const {
         uint32_t a = k0, b = k1;
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            const uint64_t gj = static_cast<G>(g + static_cast<G>(j) * step);
+            const uint64_t gj = g[j];
             w[j] = make_uint4(static_cast<uint32_t>(gj), static_cast<uint32_t>(gj >> 32), o0, o1);
         }
 #pragma unroll
@@ -46,8 +46,9 @@ struct DropoutRng {
     }
 
     __device__ __forceinline__ uint4 block(uint64_t g) const {
+        const uint64_t gs[1] = {g};
         uint4 w[1];
-        blocks<1>(g, 0, w);
+        blocks<1>(gs, w);
         return w[0];
     }
 

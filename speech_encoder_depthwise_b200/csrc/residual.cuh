@@ -41,8 +41,6 @@ template <typename T> struct Oct {
         r = make_uint4(H::pack(f[0].x, f[0].y), H::pack(f[1].x, f[1].y), H::pack(f[2].x, f[2].y),
                        H::pack(f[3].x, f[3].y));
     }
-    __device__ __forceinline__ void keep(const uint32_t (&m)[4]) { r = make_uint4(r.x & m[0], r.y & m[1], r.z & m[2], r.w & m[3]); }
-    __device__ __forceinline__ void store_shared(T *p) const { *reinterpret_cast<uint4 *>(p) = r; }
     __device__ __forceinline__ void store_global(T *p) const { *reinterpret_cast<uint4 *>(p) = r; }
     static __device__ __forceinline__ void store(T *p, const float2 (&f)[4]) {
         Oct o;
@@ -62,10 +60,6 @@ template <> struct Oct<float> {
     __device__ __forceinline__ void zero() { v[0] = v[1] = v[2] = v[3] = make_float2(0.f, 0.f); }
     __device__ __forceinline__ void get(float2 (&f)[4]) const { f[0] = v[0]; f[1] = v[1]; f[2] = v[2]; f[3] = v[3]; }
     __device__ __forceinline__ void set(const float2 (&f)[4]) { v[0] = f[0]; v[1] = f[1]; v[2] = f[2]; v[3] = f[3]; }
-    __device__ __forceinline__ void store_shared(float *p) const {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-    }
     __device__ __forceinline__ void store_global(float *p) const {
         asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0].x), "f"(v[0].y),
                      "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
@@ -87,156 +81,69 @@ __device__ __forceinline__ void load_params8(const float *p, float2 (&f)[4]) {
 }
 
 // The channels of one thread in a row kernel: NO octets, TPR apart, of a row held by TPR threads.
-// Octets lie on multiples of 8 of the flat index, so every one is an aligned word whatever C is: a row
-// starts s = (r C) mod 8 elements into its first octet, and octet v holds its channels 8 v - s ..
-// 8 v - s + 7.  SHIFT false: C is a multiple of 8, s = 0.  A thread's rows are a multiple of 8
-// apart, so it keeps its s and its channels.  A row has more than TPR (NO - 1) octets (SHIFT: may touch
-// that many), so only the last octet of a thread can lie behind the row, and only the first one
-// and the last two can be partial.
+// Octets lie on multiples of 8 of the flat index, so every one is an aligned word whatever C is: row r
+// has `head` channels before its first octet, m octets, and up to 7 channels behind them.  The
+// channels before and behind (the edges) go one each to lanes 0 .. 6 and 8 .. 14, as scalars: no
+// octet is ever partial and no neighbouring row is touched.  SHIFT false: C is a multiple of 8, no
+// edges.  A thread's rows are a multiple of 8 apart, so it keeps its channels from row to row.  A row
+// has at least TPR (NO - 1) octets, so only the last octet of a thread can lie behind them.
 template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
-    static constexpr int kGroup = TPR < 32 ? TPR : 32;  // lanes that store a row's partial octets together
-    int lane, s, C, rows;
-    bool two;                 // some lane's octet NO - 2 is partial (the same in the whole warp)
-    uint32_t mask[2][4];      // the own elements of octets 0 and NO - 1, 16 bits each
-    T *scratch;               // SHIFT: two octets of the group in shared memory
-    int cf, ce;               // the channel of the first and of the last octet that this lane stores, or -1
+    int lane, C, head, m;
+    int ce;  // the edge channel of this thread, or -1
 
-    __device__ __forceinline__ void start(int C_, int rows_, int first, T *scratch_) {
+    __device__ __forceinline__ void start(int C_, int first) {
         lane = static_cast<int>(threadIdx.x) % TPR;
         C = C_;
-        rows = rows_;
-        s = SHIFT ? static_cast<int>((static_cast<int64_t>(first) * C) % 8) : 0;
-        two = false;
+        head = 0;
+        m = C / 8;
+        ce = -1;
         if constexpr (SHIFT) {
-            scratch = scratch_ + threadIdx.x / kGroup * 16;
-            if (NO > 2) two = __any_sync(0xffffffffu, c0(NO - 2) + 8 > C);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = k ? NO - 1 : 0;
-                    mask[k][i] = (has(j, 2 * i) ? 0x0000ffffu : 0u) | (has(j, 2 * i + 1) ? 0xffff0000u : 0u);
-                }
-            const int q = lane % kGroup, vend = (C + s - 1) / 8, last = 8 * vend - s + q;
-            cf = s > 0 && lane < 8 && q >= s && q - s < C ? q - s : -1;
-            ce = (C + s) % 8 != 0 && (vend > 0 || s == 0) && q < 8 && last < C && vend % TPR / kGroup == lane / kGroup ? last : -1;
+            head = static_cast<int>(-static_cast<int64_t>(first) * C & 7);
+            if (head > C) head = C;
+            m = (C - head) / 8;
+            const int behind = head + 8 * m;
+            if (lane < head) ce = lane;
+            if (lane >= 8 && lane < 15 && behind + lane - 8 < C) ce = behind + lane - 8;
         }
     }
-    __device__ __forceinline__ int c0(int j) const { return 8 * (j * TPR + lane) - s; }
-    __device__ __forceinline__ bool any(int j) const { return j < NO - 1 || c0(j) < C; }
-    __device__ __forceinline__ bool full(int j) const {
-        if (!SHIFT || (j > 0 && j < NO - 2)) return true;
-        if (j > 0 && j == NO - 2) return !two || c0(j) + 8 <= C;
-        return c0(j) >= 0 && c0(j) + 8 <= C;
-    }
-    __device__ __forceinline__ bool has(int j, int i) const {
-        return !SHIFT || static_cast<unsigned>(c0(j) + i) < static_cast<unsigned>(C);
-    }
-    // Flat index of the thread's first octet in row r.
-    __device__ __forceinline__ int64_t at(int r) const { return static_cast<int64_t>(r) * C - s + 8 * lane; }
-    // The octets of row r, e = at(r).  Neighbouring rows' elements come along in a row's first and last
-    // octet and are ignored; the last octet of the tensor may reach past its end.
-    __device__ __forceinline__ void load_row(const T *p, int64_t e, int r, Oct<T> (&o)[NO]) const {
-        const T *q = p + e;
-        if (!SHIFT || r < rows - 1) {
-#pragma unroll
-            for (int j = 0; j < NO; ++j)
-                if (any(j)) o[j].load(q + 8 * j * TPR);
-        } else if constexpr (SHIFT) {
-#pragma unroll
-            for (int j = 0; j < NO; ++j) {
-                if (!any(j)) continue;
-                float2 f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[i].x = has(j, 2 * i) ? load1(q + 8 * j * TPR + 2 * i) : 0.f;
-                    f[i].y = has(j, 2 * i + 1) ? load1(q + 8 * j * TPR + 2 * i + 1) : 0.f;
-                }
-                o[j].set(f);
-            }
-        }
-    }
-    // A row's octets to p, by every lane of the warp (rows that are not `on` store nothing).  The
-    // elements of the partial octets go through shared memory to lanes that store one each.
-    __device__ __forceinline__ void store_row(T *p, int64_t e, bool on, const float2 (&f)[NO][4]) const {
-        T *q = p + e;
-#pragma unroll
-        for (int j = 0; j < NO; ++j) {
-            Oct<T> o;
-            o.set(f[j]);
-            if (on && any(j) && full(j)) o.store_global(q + 8 * j * TPR);
-            if constexpr (SHIFT)
-                if (!(j > 0 && j < NO - 2) && any(j) && !full(j)) o.store_shared(scratch + (j == 0 && c0(0) < 0 ? 0 : 8));
-        }
-        if constexpr (SHIFT) {
-            __syncwarp();
-            const T *row = scratch + static_cast<int>(threadIdx.x % kGroup);
-            T *base = q - (8 * lane - s);
-            if (on && cf >= 0) base[cf] = row[0];
-            if (on && ce >= 0) base[ce] = row[8];
-            __syncwarp();
-        }
-    }
-    __device__ __forceinline__ void store_zeros(T *p, int64_t e, bool on) const {
-        const float2 zero[4] = {};
-        T *q = p + e;
+    __device__ __forceinline__ int c0(int j) const { return head + 8 * (j * TPR + lane); }
+    __device__ __forceinline__ bool any(int j) const { return j < NO - 1 || j * TPR + lane < m; }
+    __device__ __forceinline__ bool edge() const { return SHIFT && ce >= 0; }
+    // Flat index of the thread's first octet in row r (a multiple of 8), and of its edge channel.
+    __device__ __forceinline__ int64_t at(int r) const { return static_cast<int64_t>(r) * C + (head + 8 * lane); }
+    __device__ __forceinline__ int64_t edge_at(int r) const { return static_cast<int64_t>(r) * C + ce; }
+    __device__ __forceinline__ void load_row(const T *p, int64_t e, Oct<T> (&o)[NO]) const {
 #pragma unroll
         for (int j = 0; j < NO; ++j)
-            if (on && any(j) && full(j)) Oct<T>::store(q + 8 * j * TPR, zero);
-        if constexpr (SHIFT) {
-            T *base = q - (8 * lane - s);
-            if (on && cf >= 0) store1(base + cf, 0.f);
-            if (on && ce >= 0) store1(base + ce, 0.f);
-        }
+            if (any(j)) o[j].load(p + e + 8 * j * TPR);
     }
-    // Octet j's values, zeros in the places that are not this row's.
-    __device__ __forceinline__ void get(int j, const Oct<T> &o, float2 (&f)[4]) const {
-        if constexpr (SHIFT && sizeof(T) == 2) {
-            Oct<T> m = o;
-            if (j == 0) m.keep(mask[0]);
-            if (j == NO - 1 && NO > 1) m.keep(mask[1]);
-            m.get(f);
-            if (NO > 2 && j == NO - 2 && two) clear_partial(j, f);
-        } else {
-            o.get(f);
-            clear_outside(j, f);
-        }
+    __device__ __forceinline__ void store_row(T *p, int64_t e, const float2 (&f)[NO][4]) const {
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+            if (any(j)) Oct<T>::store(p + e + 8 * j * TPR, f[j]);
     }
-    __device__ __forceinline__ void clear_partial(int j, float2 (&f)[4]) const {
+    __device__ __forceinline__ void store_zeros(T *p, int r) const {
+        const float2 zero[4] = {};
+        const int64_t e = at(r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!has(j, 2 * i)) f[i].x = 0.f;
-            if (!has(j, 2 * i + 1)) f[i].y = 0.f;
-        }
+        for (int j = 0; j < NO; ++j)
+            if (any(j)) Oct<T>::store(p + e + 8 * j * TPR, zero);
+        if (edge()) store1(p + edge_at(r), 0.f);
     }
-    // Zeros in the places of an octet that are not this row's.
-    __device__ __forceinline__ void clear_outside(int j, float2 (&f)[4]) const {
-        if constexpr (!SHIFT) {
-            if (j == NO - 1) {
-                const bool in = any(j);
+    // Zeros in an octet behind the row's.
+    __device__ __forceinline__ void clear_behind(int j, float2 (&f)[4]) const {
+        if (j < NO - 1) return;
+        const bool in = any(j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = in ? f[i] : make_float2(0.f, 0.f);
-            }
-        } else if (j == 0 || j == NO - 1) {
-            // an element's 16 mask bits, twice
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t m = mask[j == 0 ? 0 : 1][i];
-                f[i].x = __uint_as_float(__float_as_uint(f[i].x) & __byte_perm(m, 0, 0x1010));
-                f[i].y = __uint_as_float(__float_as_uint(f[i].y) & __byte_perm(m, 0, 0x3232));
-            }
-        } else if (j == NO - 2 && two) {
-            clear_partial(j, f);
-        }
+        for (int i = 0; i < 4; ++i) f[i] = in ? f[i] : make_float2(0.f, 0.f);
     }
 };
 
-// Parameters in shared memory for rows that start inside an octet: channel c at word
-// (c % 8) Q + c / 8 + 1.  Element i of octet v is channel 8 v + i - s, at v + off(i) with off the
-// same in every octet, so the lanes of a row read neighbouring words: no bank conflicts, and no
-// address arithmetic but an immediate.  Places without a channel hold zeros.
-__device__ __forceinline__ int shifted_q(int C) { return (C + 7) / 8 + 2; }
-__device__ __forceinline__ int shifted_off(int i, int s, int Q) { return ((i - s) & 7) * Q + (i < s ? 0 : 1); }
+// Parameters in shared memory for rows with edges: channel c at word (c % 8) Q + c / 8.  Element i of
+// octet v is channel head + 8 v + i, at v + off(i) with off the same in every octet, so the lanes
+// of a row read neighbouring words: no bank conflicts, and no address arithmetic but an immediate.
+__device__ __forceinline__ int shifted_q(int C) { return (C + 7) / 8 + 1; }
+__device__ __forceinline__ int shifted_at(int c, int Q) { return (c & 7) * Q + (c >> 3); }
 
 // The rows of one thread group: first, first + step, ..., and whether each is valid (32-bit rows).
 struct RowWalk {
@@ -280,24 +187,43 @@ struct Dropper {
         R.load(rng);
         thr16 = thr << 16;
     }
-    template <int NO> __device__ __forceinline__ void apply(uint32_t g, uint32_t step, float2 (&x)[NO][4]) const {
-        uint4 w[NO];
-        R.blocks<NO>(g, step, w);
+    __device__ __forceinline__ void clear(const uint4 &w, float2 (&x)[4]) const {
+        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < NO; ++j) {
-            const uint32_t q[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[j][i].x = (q[i] << 16) < thr16 ? 0.f : x[j][i].x;
-                x[j][i].y = q[i] < thr16 ? 0.f : x[j][i].y;
-            }
+        for (int i = 0; i < 4; ++i) {
+            x[i].x = (q[i] << 16) < thr16 ? 0.f : x[i].x;
+            x[i].y = q[i] < thr16 ? 0.f : x[i].y;
         }
+    }
+    template <int NO> __device__ __forceinline__ void apply(uint32_t g, uint32_t step, float2 (&x)[NO][4]) const {
+        uint32_t gs[NO];
+        uint4 w[NO];
+#pragma unroll
+        for (int j = 0; j < NO; ++j) gs[j] = g + j * step;
+        R.blocks<NO>(gs, w);
+#pragma unroll
+        for (int j = 0; j < NO; ++j) clear(w[j], x[j]);
+    }
+    // The same with one element more, flat index e.
+    template <int NO>
+    __device__ __forceinline__ void apply(uint32_t g, uint32_t step, float2 (&x)[NO][4], int64_t e, float &xe) const {
+        uint32_t gs[NO + 1];
+        uint4 w[NO + 1];
+#pragma unroll
+        for (int j = 0; j < NO; ++j) gs[j] = g + j * step;
+        gs[NO] = static_cast<uint32_t>(e >> 3);
+        R.blocks<NO + 1>(gs, w);
+#pragma unroll
+        for (int j = 0; j < NO; ++j) clear(w[j], x[j]);
+        const int i = static_cast<int>(e) & 7;
+        const uint32_t lo = (i & 4) ? w[NO].z : w[NO].x, hi = (i & 4) ? w[NO].w : w[NO].y, q = (i & 2) ? hi : lo;
+        if (((i & 1) ? q : q << 16) < thr16) xe = 0.f;
     }
 };
 
-// Sum over the TPR threads of a row (8, 16 or 32 lanes of a warp, or a whole block of TPR), the
-// same in all of them.  Blocks: `red` holds 2 x TPR/32 values; `flip` alternates its halves, so
-// one barrier per sum is enough.
+// Sum over the TPR threads of a row (8, 16 or 32 lanes of a warp, or TPR/32 whole warps), the same
+// in all of them.  Several warps: `red` holds 2 x TPR/32 values of the group, `flip` alternates
+// its halves, so one barrier (the group's own, number 1 + group) per sum is enough.
 __device__ __forceinline__ float2 plus(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
 __device__ __forceinline__ float plus(float a, float b) { return a + b; }
 __device__ __forceinline__ float2 shfl_xor(float2 v, int o) {
@@ -312,8 +238,8 @@ __device__ __forceinline__ V row_sum(V v, V *red, int &flip) {
     if constexpr (TPR > 32) {
         V *half = red + flip * (TPR / 32);
         flip ^= 1;
-        if (threadIdx.x % 32 == 0) half[threadIdx.x / 32] = v;
-        __syncthreads();
+        if (threadIdx.x % 32 == 0) half[threadIdx.x % TPR / 32] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / TPR), "n"(TPR) : "memory");
         v = half[0];
 #pragma unroll
         for (int w = 1; w < TPR / 32; ++w) v = plus(v, half[w]);
