@@ -70,45 +70,36 @@ layernorm_bwd_general_kernel(const ResidualArgs a) {
     }
 }
 
-// dgamma[c], dbeta[c] = the G <= 32 R partial rows' entries in a fixed order.  A block covers 32
-// entries of the 2 ceil4(C) (8 lanes of a float4) with 32 row groups; group q adds rows q, q + 32, ...
-// in order, all loads of a thread in flight at once, then the group sums are added in a fixed tree.
-constexpr int kFinalizeRows = (kMaxPartialRows + 31) / 32;
-__global__ void __launch_bounds__(256)
+// dgamma[c], dbeta[c] = the G partial rows' entries in a fixed order.  A block covers 16 entries of the
+// 2 ceil4(C) with 8 row groups; group q adds rows q, q + 8, ... in order, its loads in flight together,
+// then the 8 group sums are added in a fixed tree.  Blocks of 128 threads with 32 registers fit
+// beside the row kernel's on an SM, so they are resident and waiting when it ends.
+__global__ void __launch_bounds__(128, 16)
 layernorm_bwd_finalize_kernel(const float *__restrict__ partials, float *__restrict__ dgamma,
                               float *__restrict__ dbeta, int G, int64_t C) {
-    __shared__ float4 red[32][9];
+    __shared__ float red[8][17];
     launch_dependents();
+    const int lane = threadIdx.x % 16, q = threadIdx.x / 16;
+    const int64_t Cp = (C + 3) / 4 * 4, E = 2 * Cp, e = static_cast<int64_t>(blockIdx.x) * 16 + lane;
+    const float *p = partials + q * E + e;
+    const bool live = e < E;
     grid_dependency_wait();
-    const int lane = threadIdx.x % 8, q = threadIdx.x / 8;
-    const int64_t Cp = (C + 3) / 4 * 4, E = 2 * Cp, e = static_cast<int64_t>(blockIdx.x) * 32 + lane * 4;
-    float4 v[kFinalizeRows], s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float s = 0.f;
+    for (int r0 = 0; r0 < G; r0 += 160) {
+        float v[20];
 #pragma unroll
-    for (int i = 0; i < kFinalizeRows; ++i) {
-        const int r = q + 32 * i;
-        v[i] = e < E && r < G ? __ldg(reinterpret_cast<const float4 *>(partials + r * E + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+        for (int i = 0; i < 20; ++i) v[i] = live && r0 + q + 8 * i < G ? __ldg(p + (r0 + 8 * i) * E) : 0.f;
 #pragma unroll
-    for (int i = 0; i < kFinalizeRows; ++i) {
-        s.x += v[i].x;
-        s.y += v[i].y;
-        s.z += v[i].z;
-        s.w += v[i].w;
+        for (int i = 0; i < 20; ++i) s += v[i];
     }
     red[q][lane] = s;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const float *p = &red[0][0].x + threadIdx.x;
-        float t[32];
-#pragma unroll
-        for (int r = 0; r < 32; ++r) t[r] = p[r * 36];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-#pragma unroll
-            for (int r = 0; r + d < 32; r += 2 * d) t[r] += t[r + d];
-        const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x, c = o < Cp ? o : o - Cp;
-        float *out = o < Cp ? dgamma : dbeta;
-        if (o < E && c < C && out) out[c] = t[0];
+    if (q == 0 && live) {
+        const float t = ((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane])) +
+                        ((red[4][lane] + red[5][lane]) + (red[6][lane] + red[7][lane]));
+        const int64_t c = e < Cp ? e : e - Cp;
+        float *out = e < Cp ? dgamma : dbeta;
+        if (c < C && out) out[c] = t;
     }
 }
 
@@ -143,8 +134,8 @@ cudaError_t layernorm_bwd_launch(const ResidualArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     if (!a.dgamma && !a.dbeta) return cudaSuccess;
-    const int64_t blocks = (2 * ((a.C + 3) / 4 * 4) + 31) / 32;
-    return launch_programmatic(layernorm_bwd_finalize_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+    const int64_t blocks = (2 * ((a.C + 3) / 4 * 4) + 15) / 16;
+    return launch_programmatic(layernorm_bwd_finalize_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, s,
                                static_cast<const float *>(a.partials), a.dgamma, a.dbeta, G, a.C);
 }
 

@@ -37,7 +37,8 @@ template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(threads_for<T>(TPR, NO), 1)
 layernorm_bwd_rows_kernel(const ResidualArgs a) {
     constexpr int kThreads = threads_for<T>(TPR, NO), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3, kStages = 2;
-    constexpr int kUnits = TPR < 32 ? kThreads / 32 : GPB, kHalf = (kUnits + 1) / 2;
+    constexpr int kUnits = TPR < 32 ? kThreads / 32 : GPB;
+    static_assert(TPR <= 32 || GPB <= 15, "a named barrier per group, numbers 1 to 15");
     __shared__ float2 red_all[GPB][2 * (TPR > 32 ? TPR / 32 : 1)];
     extern __shared__ __align__(128) unsigned char smem[];
     launch_dependents();
@@ -115,7 +116,9 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
             stage_wait<kStages - 1>();
             const Oct<T> *st = stage + buf * kStageStep;
             float2 s1 = make_float2(0.f, 0.f), s2 = s1;
-            float2 gg[NO][4], xh[NO][4];
+            // xh of three and more octets is computed again from the staged x: registers for more warps
+            constexpr bool kKeep = NO <= 2;
+            float2 gg[NO][4], xh[kKeep ? NO : 1][4];
             float ge = 0.f, xhe = 0.f;
 #pragma unroll
             for (int j = 0; j < NO; ++j) {
@@ -128,7 +131,8 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
                     xo = st[j * kThreads];
                     go = st[kTensorStep + j * kThreads];
                 }
-                xo.get(xh[j]);
+                float2(&h)[4] = xh[kKeep ? j : 0];
+                xo.get(h);
                 go.get(gg[j]);
                 float2 ga[4];
                 if constexpr (SHIFT) {
@@ -140,12 +144,12 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    xh[j][i] = fmul2(fadd2(xh[j][i], both(-mean)), both(rstd));
-                    ag[j][i] = ffma2(gg[j][i], xh[j][i], ag[j][i]);
+                    h[i] = fmul2(fadd2(h[i], both(-mean)), both(rstd));
+                    ag[j][i] = ffma2(gg[j][i], h[i], ag[j][i]);
                     ab[j][i] = fadd2(ab[j][i], gg[j][i]);
                     gg[j][i] = fmul2(gg[j][i], ga[i]);
                     s1 = fadd2(s1, gg[j][i]);
-                    s2 = ffma2(gg[j][i], xh[j][i], s2);
+                    s2 = ffma2(gg[j][i], h[i], s2);
                 }
             }
             if constexpr (SHIFT) {
@@ -166,9 +170,15 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
                     float2 d[4] = {};
                     if constexpr (MODE != kPlain)
                         if (dh && ch.any(j)) st[2 * kTensorStep + j * kThreads].get(d);
+                    float2(&h)[4] = xh[kKeep ? j : 0];
+                    if constexpr (!kKeep) {
+                        st[j * kThreads].get(h);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[i] = fmul2(fadd2(h[i], both(-mean)), both(rstd));
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 t = fadd2(gg[j][i], ffma2(xh[j][i], both(-c2), both(-c1)));
+                        const float2 t = fadd2(gg[j][i], ffma2(h[i], both(-c2), both(-c1)));
                         gg[j][i] = MODE == kPlain ? fmul2(both(rstd), t) : ffma2(both(rstd), t, d[i]);
                     }
                 }
@@ -208,46 +218,39 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
     }
     if (!a.dgamma && !a.dbeta) return;
     // the units' sums by channel: dgamma at slot[at], dbeta at slot[8 Q + at].  A unit is a group, or the
-    // groups of one warp, which take turns.  Units kHalf .. store, units 0 .. kHalf-1 add to them, then
-    // the kHalf slots are added in order.
+    // groups of one warp, which take turns.  Then the units are added in order.
     const int64_t Cp = (a.C + 3) / 4 * 4;
     float *pg = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * Cp;
     float *slots = reinterpret_cast<float *>(smem);  // the stages are done with
     constexpr int kTurns = TPR < 32 ? 32 / TPR : 1;
-    const int unit = TPR < 32 ? static_cast<int>(threadIdx.x) / 32 : g;
+    float *slot = slots + (TPR < 32 ? static_cast<int>(threadIdx.x) / 32 : g) * 16 * Q;
     stage_wait<0>();
     __syncthreads();
 #pragma unroll 1
-    for (int phase = 0; phase < 2; ++phase) {
-        float *slot = slots + (phase == 0 ? unit - kHalf : unit) * 16 * Q;
-        const bool on = (phase == 0) == (unit >= kHalf);
-#pragma unroll 1
-        for (int turn = 0; turn < kTurns; ++turn) {
-            const bool add = (phase > 0 && unit + kHalf < kUnits) || turn > 0;
-            if (on && (TPR >= 32 || static_cast<int>(threadIdx.x % 32) / TPR == turn)) {
-                const auto put = [&](float *p, float vg, float vb) {
-                    p[0] = add ? p[0] + vg : vg;
-                    p[8 * Q] = add ? p[8 * Q] + vb : vb;
-                };
+    for (int turn = 0; turn < kTurns; ++turn) {
+        if (TPR >= 32 || static_cast<int>(threadIdx.x % 32) / TPR == turn) {
+            const auto put = [&](float *p, float vg, float vb) {
+                p[0] = turn > 0 ? p[0] + vg : vg;
+                p[8 * Q] = turn > 0 ? p[8 * Q] + vb : vb;
+            };
 #pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                    if (!ch.any(j)) continue;
+            for (int j = 0; j < NO; ++j) {
+                if (!ch.any(j)) continue;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        put(slot + off[i] + j * TPR, i % 2 ? ag[j][i / 2].y : ag[j][i / 2].x, i % 2 ? ab[j][i / 2].y : ab[j][i / 2].x);
-                }
-                if (ch.edge()) put(slot + shifted_at(ch.ce, Q), age, abe);
+                for (int i = 0; i < 8; ++i)
+                    put(slot + off[i] + j * TPR, i % 2 ? ag[j][i / 2].y : ag[j][i / 2].x, i % 2 ? ab[j][i / 2].y : ab[j][i / 2].x);
             }
-            if (kTurns > 1) __syncwarp();
+            if (ch.edge()) put(slot + shifted_at(ch.ce, Q), age, abe);
         }
-        __syncthreads();
+        if (kTurns > 1) __syncwarp();
     }
+    __syncthreads();
     for (int c = threadIdx.x; c < 2 * ch.C; c += kThreads) {
         const int which = c >= ch.C, k = which ? c - ch.C : c;
         const float *p = slots + which * 8 * Q + shifted_at(k, Q);
         float t = p[0];
 #pragma unroll
-        for (int q = 1; q < kHalf; ++q) t += p[q * 16 * Q];
+        for (int q = 1; q < kUnits; ++q) t += p[q * 16 * Q];
         pg[which * Cp + k] = t;
     }
 }
@@ -255,11 +258,11 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     constexpr int kThreads = threads_for<T>(TPR, NO), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3;
-    constexpr int kUnits = TPR < 32 ? kThreads / 32 : GPB, kHalf = (kUnits + 1) / 2;
+    constexpr int kUnits = TPR < 32 ? kThreads / 32 : GPB;
     const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, SHIFT, MODE>;
     const size_t words = 8 * static_cast<size_t>((a.C + 7) / 8 + 1);
     const size_t stages = 2 * static_cast<size_t>(kTensors) * NO * kThreads * sizeof(Oct<T>);
-    const size_t during = stages + (SHIFT ? words * sizeof(float) : 0), after = kHalf * 2 * words * sizeof(float);
+    const size_t during = stages + (SHIFT ? words * sizeof(float) : 0), after = kUnits * 2 * words * sizeof(float);
     const size_t smem = during > after ? during : after;
     if (smem > 226 * 1024) return cudaErrorNotSupported;
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), static_cast<int>(smem));
