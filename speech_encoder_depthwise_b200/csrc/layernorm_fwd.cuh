@@ -168,7 +168,8 @@ cudaError_t launch(const ResidualArgs &a, cudaStream_t s) {
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, 0) == cudaSuccess && n > 0 ? n : 1;
     }();
     if (SHIFT) {
-        const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), static_cast<int>(smem));
+        static SmemGrant grant;
+        const cudaError_t e = grant(reinterpret_cast<const void *>(kern), static_cast<int>(smem), -1);
         if (e != cudaSuccess) return e;
     }
     int64_t per_sm = regs_per_sm;

@@ -1,10 +1,31 @@
 // Device helpers shared by the residual-path kernels (layer norm, dropout with the residual add).
 #pragma once
 
+#include <atomic>
+
 #include "dropout.cuh"
 #include "dw_common.cuh"
 
 namespace dwk {
+
+// Dynamic shared memory beyond 48 KB, granted once per kernel, device and size (one of these per
+// kernel).  `carveout`: the share of the SM's 256 KB that is to be shared memory, in percent of
+// 228 KB (-1: what the kernel's own blocks need).
+struct SmemGrant {
+    std::atomic<int> bytes[32] = {};
+    cudaError_t operator()(const void *kern, int want, int carveout) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 32 && bytes[dev].load(std::memory_order_acquire) >= want) return cudaSuccess;
+        if (want < 48 * 1024) want = 48 * 1024;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
+        if (e == cudaSuccess && carveout >= 0)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
+        if (e == cudaSuccess && dev < 32) bytes[dev].store(want, std::memory_order_release);
+        return e;
+    }
+};
 
 // One element of any type at any alignment, as float32 and back.
 template <typename T> __device__ __forceinline__ float load1(const T *p) {
@@ -144,6 +165,8 @@ template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
 // of a row read neighbouring words: no bank conflicts, and no address arithmetic but an immediate.
 __device__ __forceinline__ int shifted_q(int C) { return (C + 7) / 8 + 1; }
 __device__ __forceinline__ int shifted_at(int c, int Q) { return (c & 7) * Q + (c >> 3); }
+// Without edges: octet v's lower four channels are the 16 bytes v, its upper four the 16 bytes Q + v.
+__device__ __forceinline__ int halves_at(int c, int Q) { return 4 * ((c >> 2 & 1) * Q + (c >> 3)) + (c & 3); }
 
 // The rows of one thread group: first, first + step, ..., and whether each is valid (32-bit rows).
 struct RowWalk {
