@@ -10,19 +10,19 @@ namespace lnb {
 
 enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual add; with dropout too
 
-// Threads of a block, one block on an SM: as many as the registers of NO octets leave room for (dgamma,
-// dbeta, xh and g: 32 registers an octet) and float32's staging area, a multiple of 128 so that the
-// four partitions of an SM hold the same number of warps, and of TPR.
+// Threads of a block, one block on an SM: as many as the registers of NO octets leave room for without
+// spills (dgamma, dbeta, xh and g: 32 registers an octet) and float32's staging area, a multiple of
+// 128 so that the four partitions of an SM hold the same number of warps, and of TPR.
 template <typename T> constexpr int threads_for(int TPR, int NO) {
     constexpr bool f32 = sizeof(T) == 4;
-    const int most = NO == 1 ? 1024 : NO == 2 ? (f32 ? 512 : 640) : NO == 3 ? (f32 && TPR > 32 ? 256 : 384) : (f32 ? 256 : 384);
+    const int most = NO == 1 ? 768 : NO == 2 ? 512 : NO == 3 ? (f32 && TPR > 32 ? 256 : 384) : (f32 ? 256 : 384);
     return most / TPR * TPR;
 }
 
 // Registers of a thread: what leaves room on every partition for one warp of 32 registers, so that the
 // finalize kernel's blocks wait on the same SMs and start at once (4.4 -> 1.6 us behind 1024 channels).
 template <typename T> constexpr int regs_for(int TPR, int NO) {
-    return (16384 - 1024) / threads_for<T>(TPR, NO) * 4 / 8 * 8;
+    return (16384 - 1024) * 4 / threads_for<T>(TPR, NO) / 8 * 8;
 }
 
 // A thread's own octets on their way from global to shared memory (cp.async): it waits for its own

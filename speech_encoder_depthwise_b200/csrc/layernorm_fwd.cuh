@@ -33,6 +33,13 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     ch.start(static_cast<int>(a.C), first);
     int off[8];
     float2 pe = make_float2(0.f, 0.f);
+    // the only row of each group on its way into L2 while the previous kernel drains (1500 rows of 512 bf16:
+    // 2.0 us instead of 2.2; with more rows a group it gains nothing)
+    if (first < rows && rows <= grid * GPB) {
+        ch.prefetch_row(x, first);
+        if (res) ch.prefetch_row(res, first);
+        if (ch.lane == 0 && a.lengths) prefetch_l2(a.lengths + first / static_cast<int>(a.T));
+    }
     grid_dependency_wait();
     if constexpr (SHIFT) {
         const int Q = shifted_q(ch.C);

@@ -138,6 +138,14 @@ template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
         for (int j = 0; j < NO; ++j)
             if (any(j)) o[j].load(p + e + 8 * j * TPR);
     }
+    // Row r's lines into L2 (before the previous kernel in the stream has completed: see prefetch_l2).
+    __device__ __forceinline__ void prefetch_row(const T *p, int r) const {
+        if (lane % (128 / (8 * static_cast<int>(sizeof(T)))) == 0) {
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+                if (any(j)) prefetch_l2(p + at(r) + 8 * j * TPR);
+        }
+    }
     __device__ __forceinline__ void store_row(T *p, int64_t e, const float2 (&f)[NO][4]) const {
 #pragma unroll
         for (int j = 0; j < NO; ++j)
