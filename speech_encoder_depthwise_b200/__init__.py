@@ -410,64 +410,80 @@ def dwconv2d_bwd_dw(x, dy, dw, dbias, lengths, stride, pads, workspace, stream=N
     _check("dwconv2d_bwd_dw", st)
 
 
-class _Operands:
-    """Checks the tensors of one call against the first one, [B, T, C], and gives their pointers.
-    All of them live on that one's device; ``call`` runs there, on ``stream`` or the device's
-    current stream."""
+# The residual path's calls are short enough for their marshalling to count (a streaming step is one
+# launch of 2 us), so these helpers look at each tensor once and keep torch's names at hand.
+_names = None
 
-    __slots__ = ("dev", "dtype", "shape", "rows", "chan", "items", "code", "f32", "i32", "i64", "first")
 
-    def __init__(self, x, name):
-        import torch
-        if not x.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        self.shape = shape = tuple(x.shape)
-        if len(shape) != 3:
-            raise ValueError(f"{name} must have shape [B, T, C], got {shape}")
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        self.dev, self.dtype, self.first = x.get_device(), x.dtype, x.data_ptr()
-        self.rows, self.chan, self.items = shape[:2], shape[2:], shape[:1]
-        self.code = _dtype_code(x)
-        self.f32, self.i32, self.i64 = torch.float32, torch.int32, torch.int64
+def _torch_names():
+    global _names
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _names = (torch.float32, torch.int32, torch.int64,
+              {torch.float32: DW_F32, torch.bfloat16: DW_BF16, torch.float16: DW_F16}, torch.cuda.current_device,
+              raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream), torch.cuda.device)
+    return _names
 
-    def ptr(self, t, name, dtype, shape):
-        if t is None:
-            return None
-        if t.get_device() != self.dev:
-            raise ValueError(f"{name} must be on cuda:{self.dev}, is on {t.device}")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
 
-    def workspace(self, t):
-        if t is None:
-            return None, 0
-        return self.ptr(t, "workspace", t.dtype, t.shape), t.numel() * t.element_size()
+def _lead(x, name):
+    """Checks a call's first tensor, [B, T, C]: (pointer, shape, dtype, dtype code, device)."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = tuple(x.shape)
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have shape [B, T, C], got {shape}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    dtype = x.dtype
+    code = (_names or _torch_names())[3].get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: bfloat16, float16 or float32")
+    return x.data_ptr(), shape, dtype, code, x.get_device()
 
-    def call(self, fn, stream, *args):
-        import torch
-        if self.dev == torch.cuda.current_device():
-            st = getattr(_lib or lib(), fn)(*args, _stream(stream))
-        else:
-            with torch.cuda.device(self.dev):
-                st = getattr(lib(), fn)(*args, _stream(stream))
-        if st != DW_OK:
-            raise DwError(fn, st)
+
+def _ptr(t, name, dev, dtype, shape):
+    """Pointer of a contiguous tensor of that device, dtype and shape (None: absent)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(fn, dev, stream, args):
+    """The C entry point on the tensors' device, on ``stream`` or that device's current stream."""
+    entry = getattr(_lib or lib(), fn)
+    if dev == _names[4]():
+        st = entry(*args, _names[5](dev) if stream is None else _stream(stream))
+    else:
+        with _names[6](dev):
+            st = entry(*args, _names[5](dev) if stream is None else _stream(stream))
+    if st != DW_OK:
+        raise DwError(fn, st)
+
+
+def _ws(t, dev):
+    if t is None:
+        return None, 0
+    return _ptr(t, "workspace", dev, t.dtype, t.shape), t.numel() * t.element_size()
 
 
 def dw_layernorm_fwd(x, gamma, beta, y, mean, rstd, lengths, eps=1e-5, stream=None):
     """y = layer norm of x over C on the valid frames (zeros elsewhere); gamma, beta, mean and rstd
     may be None."""
-    o = _Operands(x, "x")
-    ptr, f32 = o.ptr, o.f32
-    o.call("dw_layernorm_fwd", stream, o.first, ptr(gamma, "gamma", f32, o.chan), ptr(beta, "beta", f32, o.chan),
-           ptr(y, "y", o.dtype, o.shape), ptr(mean, "mean", f32, o.rows), ptr(rstd, "rstd", f32, o.rows),
-           ptr(lengths, "lengths", o.i32, o.items), *o.shape, eps, o.code)
+    px, shape, dt, code, dev = _lead(x, "x")
+    f32, i32 = _names[:2]
+    B, T, C = shape
+    _call("dw_layernorm_fwd", dev, stream,
+          (px, _ptr(gamma, "gamma", dev, f32, (C,)), _ptr(beta, "beta", dev, f32, (C,)), _ptr(y, "y", dev, dt, shape),
+           _ptr(mean, "mean", dev, f32, (B, T)), _ptr(rstd, "rstd", dev, f32, (B, T)),
+           _ptr(lengths, "lengths", dev, i32, (B,)), B, T, C, eps, code))
 
 
 def dw_layernorm_bwd_workspace_size(B, T, C) -> int:
@@ -477,56 +493,63 @@ def dw_layernorm_bwd_workspace_size(B, T, C) -> int:
 
 def dw_layernorm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, lengths, workspace, stream=None):
     """Gradients of ``dw_layernorm_fwd`` into dx and (float32 [C], either may be None) dgamma, dbeta."""
-    o = _Operands(x, "x")
-    ptr, f32 = o.ptr, o.f32
-    o.call("dw_layernorm_bwd", stream, o.first, ptr(dy, "dy", o.dtype, o.shape), ptr(gamma, "gamma", f32, o.chan),
-           ptr(mean, "mean", f32, o.rows), ptr(rstd, "rstd", f32, o.rows), ptr(dx, "dx", o.dtype, o.shape),
-           ptr(dgamma, "dgamma", f32, o.chan), ptr(dbeta, "dbeta", f32, o.chan),
-           ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code, *o.workspace(workspace))
+    px, shape, dt, code, dev = _lead(x, "x")
+    f32, i32 = _names[:2]
+    B, T, C = shape
+    _call("dw_layernorm_bwd", dev, stream,
+          (px, _ptr(dy, "dy", dev, dt, shape), _ptr(gamma, "gamma", dev, f32, (C,)),
+           _ptr(mean, "mean", dev, f32, (B, T)), _ptr(rstd, "rstd", dev, f32, (B, T)), _ptr(dx, "dx", dev, dt, shape),
+           _ptr(dgamma, "dgamma", dev, f32, (C,)), _ptr(dbeta, "dbeta", dev, f32, (C,)),
+           _ptr(lengths, "lengths", dev, i32, (B,)), B, T, C, code, *_ws(workspace, dev)))
 
 
 def dw_dropout_add_fwd(x, residual, y, rng, p, alpha, lengths, stream=None):
     """y = residual + alpha/(1-p) x on the kept elements of the valid frames, residual alone on the
     dropped ones (residual may be None); ``rng`` is a CUDA int64 tensor {seed, offset}."""
-    o = _Operands(x, "x")
-    ptr = o.ptr
-    o.call("dw_dropout_add_fwd", stream, o.first, ptr(residual, "residual", o.dtype, o.shape),
-           ptr(y, "y", o.dtype, o.shape), ptr(rng, "rng", o.i64, (2,)), p, alpha,
-           ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code)
+    px, shape, dt, code, dev = _lead(x, "x")
+    _, i32, i64 = _names[:3]
+    _call("dw_dropout_add_fwd", dev, stream,
+          (px, _ptr(residual, "residual", dev, dt, shape), _ptr(y, "y", dev, dt, shape),
+           _ptr(rng, "rng", dev, i64, (2,)), p, alpha, _ptr(lengths, "lengths", dev, i32, shape[:1]), *shape, code))
 
 
 def dw_dropout_add_bwd(dy, dx, rng, p, alpha, lengths, stream=None):
     """Gradient of ``dw_dropout_add_fwd`` with respect to x (same rng, p and alpha) into dx."""
-    o = _Operands(dy, "dy")
-    ptr = o.ptr
-    o.call("dw_dropout_add_bwd", stream, o.first, ptr(dx, "dx", o.dtype, o.shape), ptr(rng, "rng", o.i64, (2,)), p,
-           alpha, ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code)
+    pdy, shape, dt, code, dev = _lead(dy, "dy")
+    _, i32, i64 = _names[:3]
+    _call("dw_dropout_add_bwd", dev, stream,
+          (pdy, _ptr(dx, "dx", dev, dt, shape), _ptr(rng, "rng", dev, i64, (2,)), p, alpha,
+           _ptr(lengths, "lengths", dev, i32, shape[:1]), *shape, code))
 
 
 def dw_dropout_add_layernorm_fwd(x, residual, rng, p, alpha, gamma, beta, h, y, mean, rstd, lengths, eps=1e-5,
                                  stream=None):
     """h = ``dw_dropout_add_fwd``'s sum and y = its layer norm in one pass (residual, h, mean, rstd,
     gamma and beta may be None)."""
-    o = _Operands(x, "x")
-    ptr, f32 = o.ptr, o.f32
-    o.call("dw_dropout_add_layernorm_fwd", stream, o.first, ptr(residual, "residual", o.dtype, o.shape),
-           ptr(rng, "rng", o.i64, (2,)), p, alpha, ptr(gamma, "gamma", f32, o.chan), ptr(beta, "beta", f32, o.chan),
-           ptr(h, "h", o.dtype, o.shape), ptr(y, "y", o.dtype, o.shape), ptr(mean, "mean", f32, o.rows),
-           ptr(rstd, "rstd", f32, o.rows), ptr(lengths, "lengths", o.i32, o.items), *o.shape, eps, o.code)
+    px, shape, dt, code, dev = _lead(x, "x")
+    f32, i32, i64 = _names[:3]
+    B, T, C = shape
+    _call("dw_dropout_add_layernorm_fwd", dev, stream,
+          (px, _ptr(residual, "residual", dev, dt, shape), _ptr(rng, "rng", dev, i64, (2,)), p, alpha,
+           _ptr(gamma, "gamma", dev, f32, (C,)), _ptr(beta, "beta", dev, f32, (C,)), _ptr(h, "h", dev, dt, shape),
+           _ptr(y, "y", dev, dt, shape), _ptr(mean, "mean", dev, f32, (B, T)), _ptr(rstd, "rstd", dev, f32, (B, T)),
+           _ptr(lengths, "lengths", dev, i32, (B,)), B, T, C, eps, code))
 
 
 def dw_dropout_add_layernorm_bwd(dy, dh, h, gamma, mean, rstd, rng, p, alpha, dx, dresidual, dgamma, dbeta, lengths,
                                  workspace, stream=None):
     """Gradients of ``dw_dropout_add_layernorm_fwd`` from dy and dh (None: zeros) into dx, dresidual
     and (float32 [C]) dgamma, dbeta; dresidual, dgamma and dbeta may be None."""
-    o = _Operands(dy, "dy")
-    ptr, f32 = o.ptr, o.f32
-    o.call("dw_dropout_add_layernorm_bwd", stream, o.first, ptr(dh, "dh", o.dtype, o.shape),
-           ptr(h, "h", o.dtype, o.shape), ptr(gamma, "gamma", f32, o.chan), ptr(mean, "mean", f32, o.rows),
-           ptr(rstd, "rstd", f32, o.rows), ptr(rng, "rng", o.i64, (2,)), p, alpha, ptr(dx, "dx", o.dtype, o.shape),
-           ptr(dresidual, "dresidual", o.dtype, o.shape), ptr(dgamma, "dgamma", f32, o.chan),
-           ptr(dbeta, "dbeta", f32, o.chan), ptr(lengths, "lengths", o.i32, o.items), *o.shape, o.code,
-           *o.workspace(workspace))
+    pdy, shape, dt, code, dev = _lead(dy, "dy")
+    f32, i32, i64 = _names[:3]
+    B, T, C = shape
+    _call("dw_dropout_add_layernorm_bwd", dev, stream,
+          (pdy, _ptr(dh, "dh", dev, dt, shape), _ptr(h, "h", dev, dt, shape), _ptr(gamma, "gamma", dev, f32, (C,)),
+           _ptr(mean, "mean", dev, f32, (B, T)), _ptr(rstd, "rstd", dev, f32, (B, T)),
+           _ptr(rng, "rng", dev, i64, (2,)), p, alpha, _ptr(dx, "dx", dev, dt, shape),
+           _ptr(dresidual, "dresidual", dev, dt, shape), _ptr(dgamma, "dgamma", dev, f32, (C,)),
+           _ptr(dbeta, "dbeta", dev, f32, (C,)), _ptr(lengths, "lengths", dev, i32, (B,)), B, T, C, code,
+           *_ws(workspace, dev)))
 
 
 def dw_selftest_wait_timeout(done, stream=None):
