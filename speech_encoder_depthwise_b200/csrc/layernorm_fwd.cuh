@@ -181,11 +181,11 @@ cudaError_t launch(const ResidualArgs &a, cudaStream_t s) {
     }
     int64_t per_sm = regs_per_sm;
     if (SHIFT && per_sm > 220 * 1024 / static_cast<int64_t>(smem + 1024)) per_sm = 220 * 1024 / (smem + 1024);
-    const int64_t rows = a.B * a.T, most = sm_count() * per_sm * GPB;  // most: rows in flight
-    const int64_t passes = (rows + most - 1) / most;
-    int64_t grid = (rows + passes * GPB - 1) / (passes * GPB);
+    const int64_t rows = a.B * a.T, need = (rows + GPB - 1) / GPB;
+    int64_t grid = sm_count() * per_sm;
     constexpr int kMult = GPB >= 8 ? 1 : 8 / GPB;
-    if (SHIFT && passes > 1) grid = (grid + kMult - 1) / kMult * kMult;  // a group's rows stay 8 k apart
+    if (grid > need) grid = need;
+    else if (SHIFT) grid = grid / kMult * kMult;  // a group's rows stay 8 k apart
     return launch_programmatic(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, a);
 }
 
