@@ -12,17 +12,18 @@ enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual ad
 
 // Threads of a block, one block on an SM: as many as the registers of NO octets leave room for without
 // spills (dgamma, dbeta, xh and g: 32 registers an octet) and float32's staging area, a multiple of
-// 128 so that the four partitions of an SM hold the same number of warps, and of TPR.
-template <typename T> constexpr int threads_for(int TPR, int NO) {
+// 128 so that the four partitions of an SM hold the same number of warps, and of TPR.  `heavy`: edges and
+// the residual (dropout+add+ln 32x1500x1023 bf16 96 us with 256 threads, 105 with 384 and spills).
+template <typename T> constexpr int threads_for(int TPR, int NO, bool heavy) {
     constexpr bool f32 = sizeof(T) == 4;
-    const int most = NO == 1 ? 768 : NO == 2 ? 512 : NO == 3 ? (f32 && TPR > 32 ? 256 : 384) : (f32 ? 256 : 384);
+    const int most = NO == 1 ? 768 : NO == 2 ? 512 : NO == 3 ? (f32 && TPR > 32 ? 256 : 384) : (f32 || heavy ? 256 : 384);
     return most / TPR * TPR;
 }
 
 // Registers of a thread: what leaves room on every partition for one warp of 32 registers, so that the
 // finalize kernel's blocks wait on the same SMs and start at once (4.4 -> 1.6 us behind 1024 channels).
-template <typename T> constexpr int regs_for(int TPR, int NO) {
-    return (16384 - 1024) * 4 / threads_for<T>(TPR, NO) / 8 * 8;
+template <typename T> constexpr int regs_for(int TPR, int NO, bool heavy) {
+    return (16384 - 1024) * 4 / threads_for<T>(TPR, NO, heavy) / 8 * 8;
 }
 
 // A thread's own octets on their way from global to shared memory (cp.async): it waits for its own
@@ -40,9 +41,9 @@ template <int N> __device__ __forceinline__ void stage_wait() { asm volatile("cp
 // its rows; the block's groups are then added in a fixed order through shared memory into the
 // block's partial row.  SHIFT: C not a multiple of 8, or gamma missing or misaligned.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
-__global__ void __maxnreg__(regs_for<T>(TPR, NO))
+__global__ void __maxnreg__(regs_for<T>(TPR, NO, SHIFT && MODE != kPlain))
 layernorm_bwd_rows_kernel(const ResidualArgs a) {
-    constexpr int kThreads = threads_for<T>(TPR, NO), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3, kStages = 2;
+    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3, kStages = 2;
     constexpr int kUnits = TPR < 32 ? kThreads / 32 : GPB;
     static_assert(TPR <= 32 || GPB <= 15, "a named barrier per group, numbers 1 to 15");
     __shared__ float2 red_all[GPB][2 * (TPR > 32 ? TPR / 32 : 1)];
@@ -272,7 +273,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
 
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
-    constexpr int kThreads = threads_for<T>(TPR, NO), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3;
+    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3;
     constexpr int kUnits = TPR < 32 ? kThreads / 32 : GPB;
     const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, SHIFT, MODE>;
     const size_t words = 8 * static_cast<size_t>((a.C + 7) / 8 + 1);
