@@ -34,7 +34,7 @@ def lib():
         if _lib is None:
             h = ctypes.CDLL(build())
             h.oracle_philox4x32.argtypes = [_U32, _U32, _U32]
-            h.oracle_dropout_kept.argtypes = [_L, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32, _U8]
+            h.oracle_dropout_kept.argtypes = [_L, _L, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32, _U8]
             h.oracle_dropout_add.argtypes = [_D, _D, _U8, _F, _I, _L, _L, _L, _D]
             h.oracle_layernorm_fwd.argtypes = [_D, _D, _D, _I, _L, _L, _L, _F, _D, _D, _D]
             h.oracle_layernorm_bwd.argtypes = [_D, _D, _D, _D, _D, _D, _I, _L, _L, _L, _D, _D, _D]
@@ -65,10 +65,11 @@ def multiplier(p, alpha) -> float:
     return alpha * 65536.0 / (65536.0 - thr) if thr < 65536 else 0.0
 
 
-def kept(shape, seed, offset, p):
-    """Truth values: which elements of a [B, T, C] tensor the dropout keeps."""
+def kept(shape, seed, offset, p, first=0):
+    """Truth values: which elements of a [B, T, C] tensor (from flat index ``first`` on) the dropout
+    keeps."""
     out = np.zeros(int(np.prod(shape)), np.uint8)
-    lib().oracle_dropout_kept(out.size, int(seed) % 2 ** 64, int(offset) % 2 ** 64, threshold(p),
+    lib().oracle_dropout_kept(int(first), out.size, int(seed) % 2 ** 64, int(offset) % 2 ** 64, threshold(p),
                               out.ctypes.data_as(_U8))
     return out.reshape(shape).astype(bool)
 

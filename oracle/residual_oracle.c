@@ -41,19 +41,20 @@ void oracle_philox4x32(const uint32_t *ctr, const uint32_t *key, uint32_t *out)
     for (int i = 0; i < 4; ++i) out[i] = x[i];
 }
 
-/* keep[e] = 1 when element e is kept, e in [0, n). */
-void oracle_dropout_kept(int64_t n, uint64_t seed, uint64_t offset, uint32_t thr, uint8_t *keep)
+/* keep[i] = 1 when element first + i is kept, i in [0, n). */
+void oracle_dropout_kept(int64_t first, int64_t n, uint64_t seed, uint64_t offset, uint32_t thr, uint8_t *keep)
 {
     const uint32_t key[2] = {(uint32_t)seed, (uint32_t)(seed >> 32)};
     #pragma omp parallel for schedule(static)
-    for (int64_t e = 0; e < n; ++e) {
+    for (int64_t k = 0; k < n; ++k) {
+        const int64_t e = first + k;
         const uint64_t g = (uint64_t)e / 8;
         const uint32_t ctr[4] = {(uint32_t)g, (uint32_t)(g >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)};
         uint32_t out[4];
         oracle_philox4x32(ctr, key, out);
         const int i = (int)(e % 8);
         const uint32_t u = i % 2 == 0 ? (out[i / 2] & 0xFFFFu) : (out[i / 2] >> 16);
-        keep[e] = u >= thr;
+        keep[k] = u >= thr;
     }
 }
 
