@@ -30,11 +30,18 @@ bool disjoint(std::initializer_list<Region> outs, std::initializer_list<Region> 
     return true;
 }
 
-// Whether every activation lies on a boundary of 8 elements.
-bool oct_aligned(dw_dtype_t dt, std::initializer_list<const void *> acts) {
-    for (const void *p : acts)
-        if (!aligned(p, 8 * dtype_size(dt))) return false;
-    return true;
+// How many elements past a boundary of 8 every activation lies, the same for all; -1 where they differ.
+int oct_phase(dw_dtype_t dt, std::initializer_list<const void *> acts) {
+    const uintptr_t es = dtype_size(dt);
+    int phase = -1;
+    for (const void *p : acts) {
+        if (p == nullptr) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const int k = at % es == 0 ? static_cast<int>(at / es % 8) : -1;
+        if (k < 0 || (phase >= 0 && k != phase)) return -1;
+        phase = k;
+    }
+    return phase;
 }
 
 dw_status_t check_sizes(int64_t B, int64_t T, int64_t C, dw_dtype_t dt, int64_t *n) {
@@ -71,7 +78,7 @@ dw_status_t norm_fwd(dwk::ResidualArgs *a, int64_t n, float eps, dw_dtype_t dt, 
                    {a->lengths, static_cast<size_t>(a->B) * sizeof(int32_t)}}))
         return DW_ERR_INVALID_ARG;
     a->eps = eps;
-    a->vec_oct = oct_aligned(dt, {a->x, a->res, a->y, a->h});
+    a->phase = oct_phase(dt, {a->x, a->res, a->y, a->h});
     return cuda_status(dwk::layernorm_fwd_launch(*a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -90,7 +97,7 @@ dw_status_t norm_bwd(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, void *works
             a->partials = static_cast<float *>(workspace);
         }
         a->G = dwk::layernorm_bwd_partial_rows(a->B, a->T, a->C);
-        a->vec_oct = oct_aligned(dt, {a->x, a->dy, a->dh, a->dx, a->dres});
+        a->phase = oct_phase(dt, {a->x, a->dy, a->dh, a->dx, a->dres});
     }
     if (n == 0 && !params) return DW_OK;
     // with no rows only dgamma and dbeta are touched
@@ -110,7 +117,7 @@ dw_status_t dropout_add(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, dw_strea
     if (!disjoint({{a->y, act}}, {{a->x, act}, {a->res, act}, {a->rng, a->thr ? 16u : 0u},
                                   {a->lengths, static_cast<size_t>(a->B) * sizeof(int32_t)}}))
         return DW_ERR_INVALID_ARG;
-    a->vec_oct = oct_aligned(dt, {a->x, a->res, a->y});
+    a->phase = oct_phase(dt, {a->x, a->res, a->y});
     return cuda_status(dwk::dropout_add_launch(*a, static_cast<cudaStream_t>(stream)));
 }
 

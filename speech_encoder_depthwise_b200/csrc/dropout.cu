@@ -165,7 +165,7 @@ cudaError_t launch_octets(const ResidualArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t dropout_add_launch(const ResidualArgs &a, cudaStream_t s) {
-    if (a.vec_oct && a.thr < 65536 && a.B * a.T * a.C < (int64_t(1) << 35)) return with_dtype(a.dtype, [&](auto t) { return launch_octets<decltype(t)>(a, s); });
+    if (a.phase == 0 && a.thr < 65536 && a.B * a.T * a.C < (int64_t(1) << 35)) return with_dtype(a.dtype, [&](auto t) { return launch_octets<decltype(t)>(a, s); });
     const int64_t groups = (a.B * a.T * a.C + 7) / 8;
     const int64_t blocks = (groups + 255) / 256, most = static_cast<int64_t>(sm_count()) * 8;
     const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));

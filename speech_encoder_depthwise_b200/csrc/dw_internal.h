@@ -205,7 +205,7 @@ struct ResidualArgs {
     float eps = 0.f;
     int64_t B = 0, T = 0, C = 0;
     int dtype = 0;                              // 0 float32, 1 bf16, 2 fp16
-    int vec_oct = 0;                            // every activation on an 8-element boundary (16 or 32 bytes)
+    int phase = -1;                             // elements of every activation past a boundary of 8, -1: they differ
 };
 cudaError_t dropout_add_launch(const ResidualArgs &a, cudaStream_t s);
 cudaError_t layernorm_fwd_launch(const ResidualArgs &a, cudaStream_t s);

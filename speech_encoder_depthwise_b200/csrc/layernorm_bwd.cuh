@@ -39,7 +39,7 @@ template <int N> __device__ __forceinline__ void stage_wait() { asm volatile("cp
 // TPR threads hold a row's NO octets each, staged in shared memory two rows ahead of their use.
 // Every thread keeps its channels from row to row, so dgamma and dbeta add up in registers over all
 // its rows; the block's groups are then added in a fixed order through shared memory into the
-// block's partial row.  SHIFT: C not a multiple of 8, or gamma missing or misaligned.
+// block's partial row.  SHIFT: C or the tensors' address not a multiple of 8 elements, or gamma missing or misaligned.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __maxnreg__(regs_for<T>(TPR, NO, SHIFT && MODE != kPlain))
 layernorm_bwd_rows_kernel(const ResidualArgs a) {
@@ -55,7 +55,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a) {
     float2 *red = red_all[g];
     const int first = blockIdx.x + grid * g;
     Channels<T, TPR, NO, SHIFT> ch;
-    ch.start(static_cast<int>(a.C), first);
+    ch.start(static_cast<int>(a.C), first, a.phase);
     const int Q = shifted_q(ch.C);
     int off[8];
 #pragma unroll
@@ -330,9 +330,9 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, int *G, cudaStream_t
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, int *G, cudaStream_t s) {
-    if (!a.vec_oct || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u || a.B * a.T * a.C >= (int64_t(1) << 35))
+    if (a.phase < 0 || (a.phase > 0 && a.thr) || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u || a.B * a.T * a.C >= (int64_t(1) << 35))
         return cudaErrorNotSupported;
-    if (a.C % 8 == 0 && a.gamma && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0)
+    if (a.C % 8 == 0 && a.phase == 0 && a.gamma && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0)
         return launch_octets<T, false>(a, a.C / 8, G, s);
     return launch_octets<T, true>(a, a.C / 8, G, s);
 }

@@ -18,7 +18,7 @@ enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual ad
 
 // TPR threads hold a row's NO octets each in registers: one read of x (and res), the mean, then
 // the variance of the centred values, then the outputs; the next row's octets are requested first.
-// SHIFT: C not a multiple of 8, or a parameter missing or misaligned; gamma and beta then come from
+// SHIFT: C or the tensors' address not a multiple of 8 elements, or a parameter missing or misaligned; gamma and beta then come from
 // shared memory instead of L1.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(TPR, NO, sizeof(T)))
@@ -34,7 +34,7 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     float *red = red_all[g];
     const int first = blockIdx.x + grid * g;
     Channels<T, TPR, NO, SHIFT> ch;
-    ch.start(static_cast<int>(a.C), first);
+    ch.start(static_cast<int>(a.C), first, a.phase);
     int off[8];
     float2 pe = make_float2(0.f, 0.f);
     // the only row of each group on its way into L2 while the previous kernel drains (1500 rows of 512 bf16:
@@ -247,10 +247,10 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, cudaStream_t s) {
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, cudaStream_t s) {
-    if (!a.vec_oct || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u || a.B * a.T * a.C >= (int64_t(1) << 35))
+    if (a.phase < 0 || (a.phase > 0 && a.thr) || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u || a.B * a.T * a.C >= (int64_t(1) << 35))
         return cudaErrorNotSupported;
     const bool params32 = a.gamma && a.beta && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0 && reinterpret_cast<uintptr_t>(a.beta) % 32 == 0;
-    if (a.C % 8 == 0 && params32) return launch_octets<T, false>(a, a.C / 8, s);
+    if (a.C % 8 == 0 && a.phase == 0 && params32) return launch_octets<T, false>(a, a.C / 8, s);
     return launch_octets<T, true>(a, a.C / 8, s);
 }
 

@@ -102,8 +102,9 @@ __device__ __forceinline__ void load_params8(const float *p, float2 (&f)[4]) {
 }
 
 // The channels of one thread in a row kernel: NO octets, TPR apart, of a row held by TPR threads.
-// Octets lie on multiples of 8 of the flat index, so every one is an aligned word whatever C is: row r
-// has `head` channels before its first octet, m octets, and up to 7 channels behind them.  The
+// Octets lie on multiples of 8 of the flat index (counted from the `phase` elements that the tensors
+// lie past such a boundary), so every one is an aligned word whatever C is: row r has `head`
+// channels before its first octet, m octets, and up to 7 channels behind them.  The
 // channels before and behind (the edges) go one each to lanes 0 .. 6 and 8 .. 14, as scalars: no
 // octet is ever partial and no neighbouring row is touched.  SHIFT false: C is a multiple of 8, no
 // edges.  A thread's rows are a multiple of 8 apart, so it keeps its channels from row to row.  A row
@@ -112,14 +113,14 @@ template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
     int lane, C, head, m;
     int ce;  // the edge channel of this thread, or -1
 
-    __device__ __forceinline__ void start(int C_, int first) {
+    __device__ __forceinline__ void start(int C_, int first, int phase) {
         lane = static_cast<int>(threadIdx.x) % TPR;
         C = C_;
         head = 0;
         m = C / 8;
         ce = -1;
         if constexpr (SHIFT) {
-            head = static_cast<int>(-static_cast<int64_t>(first) * C & 7);
+            head = static_cast<int>(-(static_cast<int64_t>(first) * C + phase) & 7);
             if (head > C) head = C;
             m = (C - head) / 8;
             const int behind = head + 8 * m;
@@ -130,7 +131,7 @@ template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
     __device__ __forceinline__ int c0(int j) const { return head + 8 * (j * TPR + lane); }
     __device__ __forceinline__ bool any(int j) const { return j < NO - 1 || j * TPR + lane < m; }
     __device__ __forceinline__ bool edge() const { return SHIFT && ce >= 0; }
-    // Flat index of the thread's first octet in row r (a multiple of 8), and of its edge channel.
+    // Flat index of the thread's first octet in row r, and of its edge channel.
     __device__ __forceinline__ int64_t at(int r) const { return static_cast<int64_t>(r) * C + (head + 8 * lane); }
     __device__ __forceinline__ int64_t edge_at(int r) const { return static_cast<int64_t>(r) * C + ce; }
     __device__ __forceinline__ void load_row(const T *p, int64_t e, Oct<T> (&o)[NO]) const {

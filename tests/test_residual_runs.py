@@ -291,3 +291,31 @@ def test_more_rows_than_32_bit_row_kernels_take():
     assert_within("y", f64(y[:, -1000:]), ry, store("f16", ry, ey))
     assert_within("mean", f64(m[:, -1000:]), rm, em)
     assert bool((y[0, :2 ** 20] == 0).all()) and bool((y[0, -3:] == 0).all())
+
+
+@pytest.mark.parametrize("C", [64, 333])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_activations_at_different_alignments(C, dtype):
+    """Inputs and outputs that lie differently past 16-byte boundaries take the general kernels."""
+    c = Case(2, 21, C, dtype, lengths=[21, 8], seed=C)
+    acts = c.act
+    for i in range(2):
+        c.act = lambda a: (setattr(c, "offset", 1 if i == 0 else 5), acts(a), setattr(c, "offset", 0))[1]
+        c.offset = 0
+        run_ln_fwd(c)
+        run_ln_bwd(c)
+        run_dal_fwd(c, 0.2, 0.5)
+        run_dal_bwd(c, 0.2, 0.5)
+
+
+@pytest.mark.parametrize("offset", range(8))
+def test_every_phase_of_the_tensors(offset):
+    """All tensors the same number of elements past a boundary: the row kernels with edges, several rows
+    a thread group (with dropout, the general kernels)."""
+    for dtype, C in (("f16", 256), ("f32", 130), ("bf16", 1021)):
+        c = Case(2, 1500, C, dtype, lengths=[1500, 700], seed=offset, offset=offset)
+        run_ln_fwd(c)
+        run_ln_bwd(c)
+        run_dal_fwd(c, 0.0, 0.5)
+        run_dal_bwd(c, 0.0, 0.5)
+    run_dal_bwd(Case(2, 30, 200, "bf16", lengths=[30, 7], seed=offset, offset=offset), 0.2, 0.5)
