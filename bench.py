@@ -52,7 +52,8 @@ def parse():
                    help="comma list of the measurements after the step: the other workloads (sweep: causal "
                         "kernel-width sweep; sub: subsampler symmetric/causal, tensor-core and FP32 kernels; bwd: "
                         "training-size dX, dW and one-pass backward) and the NEXT rows (stream, conv2d, "
-                        "f16_packed, sub_bwd, batch); 'all' or 'none'")
+                        "f16_packed, sub_bwd, batch); 'all' or 'none'; 'residual' (layer norm, dropout with the "
+                        "residual add and the two in one pass) runs only when named")
     return p.parse_args()
 
 
@@ -383,6 +384,46 @@ def measure_f16_packed(dw, dev, hbm):
                                  "alg_bytes": by_pk}
     return {"workload": f"conformer dwconv1d forward {B}x{T}x{C}, K={K}, sym, len U[750,1500]: bf16 vs fp16 "
                         "padded, and the same sequences packed (3 rotating input sets in a CUDA graph)", **res}
+
+
+def measure_residual(dw, dev, hbm):
+    """The residual path on the conformer shape, 16x1500x512 bf16, lengths U[750,1500], p = 0.1: layer
+    norm, dropout with the residual add, and the two in one pass, forward and backward, each over 3
+    rotating input sets in a CUDA graph.  Algorithmic bytes: inputs at the valid frames, outputs in
+    full."""
+    import torch
+    B, T, C, p = 16, 1500, 512, 0.1
+    L = np.random.default_rng(1).integers(750, 1501, size=B).astype(np.int32)
+    ln = torch.from_numpy(L).to(dev)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(1)
+    act = lambda: torch.randn(B, T, C, device=dev, generator=gen).to(torch.bfloat16)
+    f32 = lambda *s: torch.empty(*s, device=dev)
+    gamma, beta = torch.rand(C, device=dev, generator=gen) + 0.5, torch.randn(C, device=dev, generator=gen)
+    rng = torch.tensor([1, 2], dtype=torch.int64, device=dev)
+    ws = torch.empty(dw.dw_layernorm_bwd_workspace_size(B, T, C), dtype=torch.uint8, device=dev)
+    dg, db = f32(C), f32(C)
+    sets = [dict(x=act(), r=act(), dy=act(), h=act(), y=act(), dx=act(), ds=act(), m=f32(B, T), rs=f32(B, T))
+            for _ in range(3)]
+    calls = {
+        "layernorm_fwd": lambda s: dw.dw_layernorm_fwd(s["r"], gamma, beta, s["y"], s["m"], s["rs"], ln),
+        "layernorm_bwd": lambda s: dw.dw_layernorm_bwd(s["r"], s["dy"], gamma, s["m"], s["rs"], s["dx"], dg, db, ln, ws),
+        "dropout_add_fwd": lambda s: dw.dw_dropout_add_fwd(s["x"], s["r"], s["y"], rng, p, 1.0, ln),
+        "dropout_add_bwd": lambda s: dw.dw_dropout_add_bwd(s["dy"], s["dx"], rng, p, 1.0, ln),
+        "dropout_add_layernorm_fwd": lambda s: dw.dw_dropout_add_layernorm_fwd(
+            s["x"], s["r"], rng, p, 1.0, gamma, beta, s["h"], s["y"], s["m"], s["rs"], ln),
+        "dropout_add_layernorm_bwd": lambda s: dw.dw_dropout_add_layernorm_bwd(
+            s["dy"], s["r"], s["h"], gamma, s["m"], s["rs"], rng, p, 1.0, s["dx"], s["ds"], dg, db, ln, ws)}
+    V, N = int(L.sum()) * C * 2, B * T * C * 2
+    by = {"layernorm_fwd": V + N, "layernorm_bwd": 2 * V + N, "dropout_add_fwd": 2 * V + N, "dropout_add_bwd": V + N,
+          "dropout_add_layernorm_fwd": 2 * V + 2 * N, "dropout_add_layernorm_bwd": 3 * V + 2 * N}
+    res = {}
+    for name, f in calls.items():
+        us = graph_us(dev, [lambda s=s: f(s) for s in sets])
+        res[name] = {"us": us, "GB_per_s": by[name] / us / 1e3, "hbm_frac_of_measured": by[name] / us / 1e3 / hbm,
+                     "alg_bytes": by[name]}
+    return {"workload": f"residual path {B}x{T}x{C} bf16, len U[750,1500], p = {p} (3 rotating input sets in a CUDA "
+                        "graph)", **res}
 
 
 def measure_batch_scaling(dw, dev, hbm):
@@ -1023,7 +1064,8 @@ def main():
                     ("conv2d", "dwconv2d", lambda: measure_conv2d(dw, dev, hbm)),
                     ("f16_packed", "f16_and_packed", lambda: measure_f16_packed(dw, dev, hbm)),
                     ("sub_bwd", "dw_subsample_bwd", lambda: measure_sub_bwd(dw, dev, hbm, fp32_tflops)),
-                    ("batch", "conv1d_batch_scaling", lambda: measure_batch_scaling(dw, dev, hbm))]
+                    ("batch", "conv1d_batch_scaling", lambda: measure_batch_scaling(dw, dev, hbm)),
+                    ("residual", "residual_path", lambda: measure_residual(dw, dev, hbm))]
         with ClockSampler(local) as clk_rows:
             configs = {name: fn() for key, name, fn in cfg_measures if key in want}
             next_rows = {name: fn() for key, name, fn in measures if key in want}
