@@ -420,8 +420,8 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
  *
  *  - x, y and the like are [B][T][C] io_dtype, channels last; gamma, beta, mean, rstd and the
  *    gradients of gamma and beta are float32, and so is the arithmetic.  Every output is
- *    written in full: frames t >= len_b as +0.0 (mean and rstd too).  Invalid frames of the
- *    inputs are never read.  No output may overlap an input or another output.
+ *    written in full: frames t >= len_b as +0.0 (mean and rstd too).  What invalid frames
+ *    of the inputs hold never matters.  No output may overlap an input or another output.
  *  - A packed batch [N][C] is B = 1, T = N with `lengths` pointing at its last offset
  *    (offsets + B): rows no sequence covers are then written as zeros.  A streaming step of B
  *    streams with one frame each is T = 1.

@@ -60,8 +60,8 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     int flip = 0;
     Oct<T> xo[NO], ro[NO];
     float xe = 0.f, re = 0.f;
-    const auto fetch = [&](const RowWalk &w) {
-        if (!w.in() || !w.valid()) return;
+    const auto fetch = [&](const RowWalk &w, bool any = false) {
+        if (!w.in() || !(any || w.valid())) return;
         const int64_t e = ch.at(w.r);
         ch.load_row(x, e, xo);
         if (MODE != kPlain && res) ch.load_row(res, e, ro);
@@ -79,7 +79,7 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     constexpr bool kAhead = NO * sizeof(T) * (MODE == kPlain ? 1 : 2) <= 16;
     RowWalk w;
     w.start(a.lengths, first, grid * GPB, rows, static_cast<int>(a.T));
-    if (kAhead) fetch(w);
+    if (kAhead) fetch(w, true);  // whatever its length says: the two loads' latencies overlap
     // groups of one warp walk together (their sums share its shuffles): until the first one is done
     int lead = TPR < 32 ? blockIdx.x + grid * (threadIdx.x / 32 * (32 / TPR)) : first;
     for (; lead < rows; lead += w.step) {

@@ -1,6 +1,6 @@
 """GPU parity of the residual path (layer norm, dropout with the residual add, the two in one
 pass; forward and backward) against the fp64 oracle, with element-wise bounds derived from the
-arithmetic (residualpin).  Masked frames of every input hold NaN and must not be read; every
+arithmetic (residualpin).  Masked frames of every input hold NaN and must not matter; every
 output lies between guard bands."""
 import numpy as np
 import pytest
