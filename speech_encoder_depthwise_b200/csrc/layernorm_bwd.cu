@@ -131,7 +131,7 @@ cudaError_t layernorm_bwd_launch(const ResidualArgs &a, cudaStream_t s) {
                                            dim3(256), 0, s, a);
             });
         }
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || G == 0) return e;  // G == 0: the row kernel wrote dgamma and dbeta
     }
     if (!a.dgamma && !a.dbeta) return cudaSuccess;
     const int64_t blocks = (2 * ((a.C + 3) / 4 * 4) + 15) / 16;

@@ -173,7 +173,7 @@ template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 cudaError_t launch(const ResidualArgs &a, cudaStream_t s) {
     constexpr int GPB = kThreads / TPR;
     const auto kern = layernorm_fwd_rows_kernel<T, TPR, NO, SHIFT, MODE>;
-    const size_t smem = SHIFT ? 8 * ((a.C + 7) / 8 + 1) * sizeof(float2) : 0;
+    const size_t smem = SHIFT ? 8 * shifted_q(static_cast<int>(a.C)) * sizeof(float2) : 0;
     static const int regs_per_sm = [&] {
         int n = 0;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, 0) == cudaSuccess && n > 0 ? n : 1;

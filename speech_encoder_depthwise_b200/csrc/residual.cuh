@@ -172,7 +172,8 @@ template <typename T, int TPR, int NO, bool SHIFT> struct Channels {
 // Parameters in shared memory for rows with edges: channel c at word (c % 8) Q + c / 8.  Element i of
 // octet v is channel head + 8 v + i, at v + off(i) with off the same in every octet, so the lanes
 // of a row read neighbouring words: no bank conflicts, and no address arithmetic but an immediate.
-__device__ __forceinline__ int shifted_q(int C) { return (C + 7) / 8 + 1; }
+// Q is 4 more than a multiple of 8, so that neighbouring channels lie in different banks as well.
+__host__ __device__ __forceinline__ int shifted_q(int C) { return ((C + 7) / 8 + 3) / 8 * 8 + 4; }
 __device__ __forceinline__ int shifted_at(int c, int Q) { return (c & 7) * Q + (c >> 3); }
 // Without edges: octet v's lower four channels are the 16 bytes v, its upper four the 16 bytes Q + v.
 __device__ __forceinline__ int halves_at(int c, int Q) { return 4 * ((c >> 2 & 1) * Q + (c >> 3)) + (c & 3); }
