@@ -36,7 +36,8 @@ struct DropoutRng {
         for (int r = 0; r < 10; ++r) {
 #pragma unroll
             for (int j = 0; j < NO; ++j) {
-                const uint64_t p = static_cast<uint64_t>(w[j].x) * 0xD2511F53u, q = static_cast<uint64_t>(w[j].z) * 0xCD9E8D57u;
+                const uint64_t p = static_cast<uint64_t>(w[j].x) * 0xD2511F53u;
+                const uint64_t q = static_cast<uint64_t>(w[j].z) * 0xCD9E8D57u;
                 w[j] = make_uint4(static_cast<uint32_t>(q >> 32) ^ w[j].y ^ a, static_cast<uint32_t>(q),
                                   static_cast<uint32_t>(p >> 32) ^ w[j].w ^ b, static_cast<uint32_t>(p));
             }

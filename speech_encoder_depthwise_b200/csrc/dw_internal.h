@@ -207,6 +207,13 @@ struct ResidualArgs {
     int dtype = 0;                              // 0 float32, 1 bf16, 2 fp16
     int phase = -1;                             // elements of every activation past a boundary of 8, -1: they differ
 };
+// Whether the row kernels' index ranges and alignment cover a call: 32-bit rows and octet numbers, every
+// tensor the same number of elements past an 8-element boundary, none where a mask is drawn (a mask
+// block would straddle two words), and something to keep.
+inline bool row_kernels_serve(const ResidualArgs &a) {
+    return a.phase >= 0 && (a.phase == 0 || a.thr == 0) && a.thr < 65536u && a.B * a.T < (int64_t(1) << 30) &&
+           a.B * a.T * a.C < (int64_t(1) << 35);
+}
 cudaError_t dropout_add_launch(const ResidualArgs &a, cudaStream_t s);
 cudaError_t layernorm_fwd_launch(const ResidualArgs &a, cudaStream_t s);
 // The kernels that hold a row in registers; cudaErrorNotSupported where they do not serve.

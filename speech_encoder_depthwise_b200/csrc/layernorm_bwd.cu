@@ -15,8 +15,9 @@ namespace {
 // Partial rows: at most two blocks on each of 148 SMs, and at most 64 MiB of them (at least one).
 constexpr int kMaxPartialRows = 296;
 
-// Any C, any alignment: a block per row, two passes over it; the block's partial row lives in the
-// workspace (a thread only touches its own columns, so no synchronization is needed).
+// Any C, any alignment: a block per row, two passes over it, one element at a time; the block's
+// partial row lives in the workspace (a thread only touches its own columns, so no synchronization is
+// needed).  4096 rows of 12288 bf16: 666 us (0.07 of the measured copy bandwidth).
 template <typename T>
 __global__ void __launch_bounds__(256)
 layernorm_bwd_general_kernel(const ResidualArgs a) {

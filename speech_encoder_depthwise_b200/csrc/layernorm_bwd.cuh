@@ -16,7 +16,10 @@ enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual ad
 // the residual (dropout+add+ln 32x1500x1023 bf16 96 us with 256 threads, 105 with 384 and spills).
 template <typename T> constexpr int threads_for(int TPR, int NO, bool heavy) {
     constexpr bool f32 = sizeof(T) == 4;
-    const int most = NO == 1 ? 768 : NO == 2 ? 512 : NO == 3 ? (f32 && TPR > 32 ? 256 : 384) : (f32 || heavy ? 256 : 384);
+    const int most = NO == 1   ? 768
+                     : NO == 2 ? 512
+                     : NO == 3 ? (f32 && TPR > 32 ? 256 : 384)
+                               : (f32 || heavy ? 256 : 384);
     return most / TPR * TPR;
 }
 
@@ -31,10 +34,13 @@ template <typename T> constexpr int regs_for(int TPR, int NO, bool heavy) {
 template <typename T> __device__ __forceinline__ void stage_octet(void *dst, const T *src) {
     const uint32_t d = smem_addr(dst);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-    if constexpr (sizeof(T) == 4) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + 16), "l"(src + 4) : "memory");
+    if constexpr (sizeof(T) == 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + 16), "l"(src + 4) : "memory");
 }
 __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <int N> __device__ __forceinline__ void stage_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Thread-block clusters: all blocks arrived, and a float of another block's shared memory.
 __device__ __forceinline__ void cluster_sync() {
@@ -52,19 +58,30 @@ constexpr int kCluster = 8;
 // TPR threads hold a row's NO octets each, staged in shared memory two rows ahead of their use.
 // Every thread keeps its channels from row to row, so dgamma and dbeta add up in registers over all
 // its rows; the block's groups are then added in a fixed order through shared memory into the
-// block's partial row.  FEW rows: the grid is one cluster of 8 blocks, which adds its blocks' rows
-// itself (in order, through distributed shared memory) and writes dgamma and dbeta.  SHIFT: C or the tensors' address not a multiple of 8 elements, or gamma missing or misaligned.
+// block's partial row.  `few` rows: the grid is one cluster of 8 blocks, which adds its blocks' rows
+// itself (in order, through distributed shared memory) and writes dgamma and dbeta.  SHIFT: C or the
+// tensors' address not a multiple of 8 elements, or gamma missing or misaligned.
+//
+// Bound by HBM for long batches; staged copies cost no registers, which dgamma and dbeta take (rows
+// of 2048 bf16, 32x1500: 84.5 us, 196 with a block of 256 loading one row at a time).  Measured (graph
+// replay, cold inputs, finalize included; fraction of the measured copy bandwidth): 32x1500x2048
+// bf16 84.5 us (0.89), with dropout and residual 32x1500x1024 bf16 76.9 us (0.83) and 16x1500x512
+// bf16 22.7 us (0.70), 16x1500x512 bf16 15.7 us (0.60), 8x733x519 float32 12.4 us (0.38).  The
+// small ones pay about 3 us for the two sums after the last row (block 1.2 us, finalize 1.6 us)
+// beside launch and first load.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __maxnreg__(regs_for<T>(TPR, NO, SHIFT && MODE != kPlain))
 layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
-    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3, kStages = 2;
+    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR;
+    constexpr int kTensors = MODE == kPlain ? 2 : 3, kStages = 2;
     constexpr int kUnits = TPR < 32 && !SHIFT ? kThreads / 32 : GPB;
     static_assert(TPR <= 32 || GPB <= 15, "a named barrier per group, numbers 1 to 15");
     __shared__ float2 red_all[GPB][2 * (TPR > 32 ? TPR / 32 : 1)];
     extern __shared__ __align__(128) unsigned char smem[];
     launch_dependents();
     const int g = threadIdx.x / TPR, grid = gridDim.x, rows = static_cast<int>(a.B * a.T);
-    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy), *dh = MODE == kPlain ? nullptr : static_cast<const T *>(a.dh);
+    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+    const T *dh = MODE == kPlain ? nullptr : static_cast<const T *>(a.dh);
     T *dx = static_cast<T *>(a.dx), *dres = MODE == kPlain ? nullptr : static_cast<T *>(a.dres);
     float2 *red = red_all[g];
     const int first = blockIdx.x + grid * g;
@@ -86,7 +103,9 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
     pipe.start(a.lengths, first, grid * GPB, rows, static_cast<int>(a.T));
     uint32_t valid = 0;  // bit i: row i from the one at hand is valid
     float mean_q[kStages] = {}, rstd_q[kStages] = {}, xe_q[kStages] = {}, ge_q[kStages] = {}, he_q[kStages] = {};
-    const auto request = [&](int buf, int slot) {  // buf: stage; slot: place in the queues and valid
+    // buf: stage; slot: place in the queues and in valid.  Nothing is staged for a masked row: its copies,
+    // which nobody waits for, could land after the next ones into the same stage.
+    const auto request = [&](int buf, int slot) {
         if (pipe.in() && pipe.valid()) {
             valid |= 1u << slot;
             const int64_t e = ch.at(pipe.r);
@@ -163,12 +182,14 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
                 if constexpr (SHIFT) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        ga[i] = ch.any(j) ? make_float2(sp[off[2 * i] + j * TPR], sp[off[2 * i + 1] + j * TPR]) : make_float2(0.f, 0.f);
+                        ga[i] = ch.any(j) ? make_float2(sp[off[2 * i] + j * TPR], sp[off[2 * i + 1] + j * TPR])
+                                          : make_float2(0.f, 0.f);
                 } else if constexpr (!kShared) {
                     load_params8(a.gamma + (ch.any(j) ? ch.c0(j) : 0), ga);
                 } else {
                     const int v = ch.any(j) ? j * TPR + ch.lane : 0;
-                    const float4 p = reinterpret_cast<const float4 *>(sp)[v], q = reinterpret_cast<const float4 *>(sp)[Q + v];
+                    const float4 p = reinterpret_cast<const float4 *>(sp)[v];
+                    const float4 q = reinterpret_cast<const float4 *>(sp)[Q + v];
                     ga[0] = make_float2(p.x, p.y); ga[1] = make_float2(p.z, p.w);
                     ga[2] = make_float2(q.x, q.y); ga[3] = make_float2(q.z, q.w);
                 }
@@ -309,7 +330,8 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
 
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
-    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR, kTensors = MODE == kPlain ? 2 : 3;
+    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR;
+    constexpr int kTensors = MODE == kPlain ? 2 : 3;
     constexpr int kUnits = TPR < 32 && !SHIFT ? kThreads / 32 : GPB;
     const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, SHIFT, MODE>;
     const size_t words = 8 * static_cast<size_t>(shifted_q(static_cast<int>(a.C)));
@@ -319,9 +341,11 @@ cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     if (smem > 226 * 1024) return cudaErrorNotSupported;
     // a carve-out with room for a finalize block beside this one (519 float32 channels: 5.0 us for 148 rows
     // instead of 7.6), the rest left to L1
-    const int share = static_cast<int>((smem + sizeof(float2) * GPB * 2 * (TPR > 32 ? TPR / 32 : 1) + 4096) * 100 / (228 * 1024)) + 1;
+    const size_t all = smem + sizeof(float2) * GPB * 2 * (TPR > 32 ? TPR / 32 : 1) + 4096;
+    const int share = static_cast<int>(all * 100 / (228 * 1024)) + 1;
     static SmemGrant grant;
-    const cudaError_t e = grant(reinterpret_cast<const void *>(kern), static_cast<int>(smem), share < 100 ? share : 100);
+    const cudaError_t e =
+        grant(reinterpret_cast<const void *>(kern), static_cast<int>(smem), share < 100 ? share : 100);
     if (e != cudaSuccess) return e;
     const int64_t rows = a.B * a.T;
     // one launch instead of two where half of one cluster's groups hold every row: the same time on the GPU
@@ -384,8 +408,7 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, int *G, cudaStream_t
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, int *G, cudaStream_t s) {
-    if (a.phase < 0 || (a.phase > 0 && a.thr) || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u || a.B * a.T * a.C >= (int64_t(1) << 35))
-        return cudaErrorNotSupported;
+    if (!row_kernels_serve(a)) return cudaErrorNotSupported;
     if (a.C % 8 == 0 && a.phase == 0 && a.gamma && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0)
         return launch_octets<T, false>(a, a.C / 8, G, s);
     return launch_octets<T, true>(a, a.C / 8, G, s);

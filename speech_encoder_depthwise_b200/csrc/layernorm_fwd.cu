@@ -9,7 +9,8 @@ namespace dwk {
 namespace {
 
 // Any C, any alignment: a block per row, three passes over the row (the second and third hit L1/L2),
-// s computed anew in each.
+// s computed anew in each, one element at a time.  Bound by instructions: 4096 rows of 12288 bf16
+// 261 us (0.12 of the measured copy bandwidth), with dropout a whole mask block per element and pass.
 template <typename T>
 __global__ void __launch_bounds__(256)
 layernorm_fwd_general_kernel(const ResidualArgs a) {
@@ -51,7 +52,8 @@ layernorm_fwd_general_kernel(const ResidualArgs a) {
         for (int64_t c = threadIdx.x; c < a.C; c += 256) {
             const float v = sum_at(c);
             if (h) store1(h + base + c, v);
-            store1(y + base + c, fmaf((v - mean) * rstd, a.gamma ? __ldg(a.gamma + c) : 1.f, a.beta ? __ldg(a.beta + c) : 0.f));
+            const float ga = a.gamma ? __ldg(a.gamma + c) : 1.f, be = a.beta ? __ldg(a.beta + c) : 0.f;
+            store1(y + base + c, fmaf((v - mean) * rstd, ga, be));
         }
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[r] = mean;

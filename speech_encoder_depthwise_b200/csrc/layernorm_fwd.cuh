@@ -12,14 +12,25 @@ constexpr int kThreads = 256;
 
 // Three blocks where their 80 registers a thread suffice without spills (32x1500x255 bf16 13.4 us instead
 // of 16.2); float32 and the wider shapes of few rows lose by it (1500 rows of 512 2.5 / 2.0 us).
-constexpr int blocks_per_sm(int TPR, int NO, int element) { return NO == 1 || (NO == 2 && TPR <= 16 && element == 2) ? 3 : 2; }
+constexpr int blocks_per_sm(int TPR, int NO, int element) {
+    return NO == 1 || (NO == 2 && TPR <= 16 && element == 2) ? 3 : 2;
+}
 
 enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual add; with dropout too
 
 // TPR threads hold a row's NO octets each in registers: one read of x (and res), the mean, then
 // the variance of the centred values, then the outputs; the next row's octets are requested first.
-// SHIFT: C or the tensors' address not a multiple of 8 elements, or a parameter missing or misaligned; gamma and beta then come from
-// shared memory instead of L1.
+// SHIFT: C or the tensors' address not a multiple of 8 elements, or a parameter missing or misaligned;
+// gamma and beta then come from shared memory instead of L1.
+//
+// Bound by HBM: 8 flops an element against 4 bytes.  What it took to get there was instructions, not
+// bytes in flight (a ring of bulk copies four rows deep was slower than plain loads): packed float32
+// arithmetic, rows shared by half a warp so that two rows share one reduction's shuffles, modes and
+// widths as instances instead of branches: 413 -> 140 instructions a row of 512 bf16.
+// Measured (graph replay, cold inputs; fraction of the measured copy bandwidth): 64x3000x1024 bf16
+// 111.6 us (0.94), 32x1500x1024 float32 56.6 us (0.93), 16x1500x512 bf16 10.0 us (0.66: about 3.5 us
+// of launch, first load and last store), 64 rows of 512 1.6 us; with dropout and residual 32x1500x1024
+// bf16 60.3 us (0.87), 16x1499x1023 fp16 36.6 us (0.72).
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(TPR, NO, sizeof(T)))
 layernorm_fwd_rows_kernel(const ResidualArgs a) {
@@ -247,9 +258,9 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, cudaStream_t s) {
 // cudaErrorNotSupported: no row kernel for these sizes or this alignment.
 template <typename T>
 cudaError_t launch_rows(const ResidualArgs &a, cudaStream_t s) {
-    if (a.phase < 0 || (a.phase > 0 && a.thr) || a.B * a.T >= (int64_t(1) << 30) || a.thr >= 65536u || a.B * a.T * a.C >= (int64_t(1) << 35))
-        return cudaErrorNotSupported;
-    const bool params32 = a.gamma && a.beta && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0 && reinterpret_cast<uintptr_t>(a.beta) % 32 == 0;
+    if (!row_kernels_serve(a)) return cudaErrorNotSupported;
+    const bool params32 = a.gamma && a.beta && reinterpret_cast<uintptr_t>(a.gamma) % 32 == 0 &&
+                          reinterpret_cast<uintptr_t>(a.beta) % 32 == 0;
     if (a.C % 8 == 0 && a.phase == 0 && params32) return launch_octets<T, false>(a, a.C / 8, s);
     return launch_octets<T, true>(a, a.C / 8, s);
 }
