@@ -425,9 +425,10 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
  *  - A packed batch [N][C] is B = 1, T = N with `lengths` pointing at its last offset
  *    (offsets + B): rows no sequence covers are then written as zeros.  A streaming step of B
  *    streams with one frame each is T = 1.
- *  - Any C from 1 to 4,194,304 and any alignment.  Activations on 16-byte boundaries take the
- *    vector kernels for every C up to 8192 channels (4096 of float32), whether or not the rows
- *    after the first start on 16 bytes; other calls take a narrower (slower) kernel.
+ *  - Any C from 1 to 4,194,304 and any alignment.  Up to 8199 channels take the vector kernels when
+ *    all activations of a call lie the same number of elements past a boundary of 8 elements (none
+ *    where a mask is drawn), whether or not the rows after the first start on 16 bytes; other
+ *    calls take a narrower (slower) kernel.
  *  - Dropout: rng points at two device uint64, {seed, offset}, read when the kernel runs, so a
  *    captured graph draws new numbers once the program changes them on the device.  Element e
  *    of the tensor (its flat index, from 0) uses the 16 bits number e mod 8 (word (e mod 8)/2,
@@ -435,8 +436,8 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
  *    (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011).  It is
  *    dropped when they are below thr = floor(65536 p + 1/2): p is rounded to a multiple of 2^-16.
  *    A dropped element counts as zero whatever it holds; a kept one is multiplied by
- *    m = alpha 65536 / (65536 - thr) (0 when thr = 65536), so the rounding of p leaves the mean
- *    of the sum as it is.  No mask is stored: the backward pass draws it again from the same rng
+ *    m = alpha 65536 / (65536 - thr) (0 when thr = 65536), so the expectation is alpha x whatever
+ *    the rounding of p.  No mask is stored: the backward pass draws it again from the same rng
  *    values, p and sizes.  alpha is the residual branch's factor (1, or 1/2 for a half-step
  *    module).  0 <= p <= 1; with thr = 0 nothing is drawn and rng may be NULL.
  */
