@@ -427,8 +427,9 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
  *    streams with one frame each is T = 1.
  *  - Any C from 1 to 4,194,304 and any alignment.  Up to 8199 channels take the vector kernels when
  *    all activations of a call lie the same number of elements past a boundary of 8 elements (none
- *    where a mask is drawn), whether or not the rows after the first start on 16 bytes; other
- *    calls take a narrower (slower) kernel.
+ *    where a mask is drawn), whether or not the rows after the first start on 16 bytes; so do
+ *    longer rows of a multiple of 8 channels, up to 51200 (backward 25600), on such a boundary.
+ *    Other calls take a narrower (slower) kernel.
  *  - Dropout: rng points at two device uint64, {seed, offset}, read when the kernel runs, so a
  *    captured graph draws new numbers once the program changes them on the device.  Element e
  *    of the tensor (its flat index, from 0) uses the 16 bits number e mod 8 (word (e mod 8)/2,

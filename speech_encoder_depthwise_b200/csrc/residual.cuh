@@ -106,6 +106,18 @@ __device__ __forceinline__ void load_params8(const float *p, float2 (&f)[4]) {
                  : "l"(p) : "memory");
 }
 
+// The same of any alignment; `missing` where there is no parameter.
+__device__ __forceinline__ void any_params8(const float *p, float missing, int64_t c, float2 (&f)[4]) {
+    if (p == nullptr) {
+        f[0] = f[1] = f[2] = f[3] = both(missing);
+    } else if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+        load_params8(p + c, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(__ldg(p + c + 2 * i), __ldg(p + c + 2 * i + 1));
+    }
+}
+
 // The channels of one thread in a row kernel: NO octets, TPR apart, of a row held by TPR threads.
 // Octets lie on multiples of 8 of the flat index (counted from the `phase` elements that the tensors
 // lie past such a boundary), so every one is an aligned word whatever C is: row r has `head`

@@ -319,3 +319,17 @@ def test_every_phase_of_the_tensors(offset):
         run_dal_fwd(c, 0.0, 0.5)
         run_dal_bwd(c, 0.0, 0.5)
     run_dal_bwd(Case(2, 30, 200, "bf16", lengths=[30, 7], seed=offset, offset=offset), 0.2, 0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("C,rows", [(8200, 700), (12288, 400), (25600, 310), (25608, 6), (51200, 6), (51208, 6)])
+def test_rows_beyond_the_register_kernels(C, rows, dtype):
+    """Rows in shared memory (forward to 51200 channels, backward to 25600) and past it."""
+    c = Case(2, rows // 2, C, dtype, lengths=[rows // 2, rows // 3], seed=C)
+    run_ln_fwd(c)
+    run_ln_fwd(c, gamma=False)
+    run_ln_bwd(c)
+    run_dal_fwd(c, 0.2, 0.5)
+    run_dal_fwd(c, 0.2, 0.5, residual=False, h=False)
+    run_dal_bwd(c, 0.2, 0.5)
+    run_dal_bwd(c, 0.0, 1.0, dh=False, gamma=False, dbeta=False)
