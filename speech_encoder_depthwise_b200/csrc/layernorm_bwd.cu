@@ -76,7 +76,8 @@ layernorm_bwd_general_kernel(const ResidualArgs a) {
 // 25600 channels): a block per row, every thread on octets of its own; the second pass reads x and dy
 // again (L2).  4096 rows of 12288 bf16 123 us (0.37 of the measured copy bandwidth, general kernel 666 us);
 // 2048 with dropout and dh 84 us (0.46); 1024 rows of 25600, one block per SM, 111 us (0.22).  Bound by the
-// wait for the loads: a row has few octets per thread.
+// wait for the loads: a row has few octets per thread.  Two or three octets at a time, as in the forward,
+// spill at the 64 registers of two blocks per SM and are slower (136 and 152 us).
 constexpr int kWideThreads = 512;
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads, 2)
