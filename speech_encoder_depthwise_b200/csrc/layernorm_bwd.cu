@@ -44,7 +44,7 @@ layernorm_bwd_general_kernel(const ResidualArgs a) {
             }
             continue;
         }
-        const float mean = __ldg(a.mean + r), rstd = __ldg(a.rstd + r);
+        const float mean = a.mean[r], rstd = a.rstd[r];
         float2 acc = make_float2(0.f, 0.f);
         for (int64_t c = threadIdx.x; c < a.C; c += 256) {
             const float xh = (load1(x + base + c) - mean) * rstd, d = load1(dy + base + c);
@@ -108,7 +108,7 @@ layernorm_bwd_wide_kernel(const ResidualArgs a) {
             }
             continue;
         }
-        const float mean = __ldg(a.mean + r), rstd = __ldg(a.rstd + r);
+        const float mean = a.mean[r], rstd = a.rstd[r];
         float2 s1 = make_float2(0.f, 0.f), s2 = s1;
         for (int v = threadIdx.x; v < n; v += kWideThreads) {
             Oct<T> xo, go;
@@ -187,7 +187,8 @@ cudaError_t launch_wide(const ResidualArgs &a, int *G, cudaStream_t s) {
 // dgamma[c], dbeta[c] = the G partial rows' entries in a fixed order.  A block covers 16 entries of the
 // 2 ceil4(C) with 8 row groups; group q adds rows q, q + 8, ... in order, its loads in flight together,
 // then the 8 group sums are added in a fixed tree.  Blocks of 128 threads with 32 registers fit
-// beside the row kernel's on an SM, so they are resident and waiting when it ends.
+// beside the row kernel's on an SM, so they are resident and waiting when it ends (and read the partial
+// rows, written meanwhile, from L2).
 __global__ void __launch_bounds__(128, 16)
 layernorm_bwd_finalize_kernel(const float *__restrict__ partials, float *__restrict__ dgamma,
                               float *__restrict__ dbeta, int G, int64_t C) {
@@ -202,7 +203,7 @@ layernorm_bwd_finalize_kernel(const float *__restrict__ partials, float *__restr
     for (int r0 = 0; r0 < G; r0 += 160) {
         float v[20];
 #pragma unroll
-        for (int i = 0; i < 20; ++i) v[i] = live && r0 + q + 8 * i < G ? __ldg(p + (r0 + 8 * i) * E) : 0.f;
+        for (int i = 0; i < 20; ++i) v[i] = live && r0 + q + 8 * i < G ? __ldcg(p + (r0 + 8 * i) * E) : 0.f;
 #pragma unroll
         for (int i = 0; i < 20; ++i) s += v[i];
     }

@@ -118,8 +118,8 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
                 if constexpr (MODE != kPlain)
                     if (dh) stage_octet(st + 2 * kTensorStep + j * kThreads, dh + e + 8 * j * TPR);
             }
-            mean_q[slot] = __ldg(a.mean + pipe.r);
-            rstd_q[slot] = __ldg(a.rstd + pipe.r);
+            mean_q[slot] = a.mean[pipe.r];
+            rstd_q[slot] = a.rstd[pipe.r];
             if (ch.edge()) {
                 xe_q[slot] = load1(x + ch.edge_at(pipe.r));
                 ge_q[slot] = load1(dy + ch.edge_at(pipe.r));

@@ -33,13 +33,7 @@ struct SmemGrant {
 };
 
 // One element of any type at any alignment, as float32 and back.
-template <typename T> __device__ __forceinline__ float load1(const T *p) {
-    Vec<T, 1> v;
-    float2 f[1];
-    v.load(p);
-    v.to_f2(f);
-    return f[0].x;
-}
+template <typename T> __device__ __forceinline__ float load1(const T *p) { return static_cast<float>(*p); }
 template <typename T> __device__ __forceinline__ void store1(T *p, float v) {
     const float2 f[1] = {make_float2(v, 0.f)};
     Vec<T, 1>::store(p, f);
@@ -51,12 +45,13 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Eight consecutive elements, moved with one instruction (16 bytes of a 16-bit type, 32 of float32):
 // the unit of the row kernels, and one block of the dropout generator.  Loads do not allocate in
-// L1 (every activation is read once), which leaves it to gamma and beta.
+// L1 (every activation is read once), which leaves it to gamma and beta, nor take the read-only path:
+// the previous kernel in the stream may write them while this one is already resident.
 template <typename T> struct Oct {
     using H = Half16<T>;
     uint4 r;
     __device__ __forceinline__ void load(const T *p) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
     }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
@@ -78,7 +73,7 @@ template <typename T> struct Oct {
 template <> struct Oct<float> {
     float2 v[4];
     __device__ __forceinline__ void load(const float *p) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y),
                        "=f"(v[3].x), "=f"(v[3].y)
                      : "l"(p) : "memory");
