@@ -102,7 +102,10 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
     RowWalk pipe;
     pipe.start(a.lengths, first, grid * GPB, rows, static_cast<int>(a.T));
     uint32_t valid = 0;  // bit i: row i from the one at hand is valid
-    float mean_q[kStages] = {}, rstd_q[kStages] = {}, xe_q[kStages] = {}, ge_q[kStages] = {}, he_q[kStages] = {};
+    float mean_q[kStages] = {}, rstd_q[kStages] = {};
+    T xe_q[kStages], ge_q[kStages], he_q[kStages];  // as loaded: a conversion here would wait for the load
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) xe_q[i] = ge_q[i] = he_q[i] = zero1<T>();
     // buf: stage; slot: place in the queues and in valid.  Nothing is staged for a masked row: its copies,
     // which nobody waits for, could land after the next ones into the same stage.
     const auto request = [&](int buf, int slot) {
@@ -121,9 +124,9 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
             mean_q[slot] = a.mean[pipe.r];
             rstd_q[slot] = a.rstd[pipe.r];
             if (ch.edge()) {
-                xe_q[slot] = load1(x + ch.edge_at(pipe.r));
-                ge_q[slot] = load1(dy + ch.edge_at(pipe.r));
-                if (MODE != kPlain && dh) he_q[slot] = load1(dh + ch.edge_at(pipe.r));
+                xe_q[slot] = x[ch.edge_at(pipe.r)];
+                ge_q[slot] = dy[ch.edge_at(pipe.r)];
+                if (MODE != kPlain && dh) he_q[slot] = dh[ch.edge_at(pipe.r)];
             }
         }
         stage_commit();
@@ -205,10 +208,11 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
             }
             if constexpr (SHIFT) {
                 if (ch.edge() && live) {
-                    xhe = (xe_q[0] - mean) * rstd;
-                    age = fmaf(ge_q[0], xhe, age);
-                    abe += ge_q[0];
-                    ge = ge_q[0] * gamma_e;
+                    const float dye = load1(ge_q);
+                    xhe = (load1(xe_q) - mean) * rstd;
+                    age = fmaf(dye, xhe, age);
+                    abe += dye;
+                    ge = dye * gamma_e;
                     s1.x += ge;
                     s2.x = fmaf(ge, xhe, s2.x);
                 }
@@ -234,7 +238,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
                     }
                 }
                 float de = 0.f;
-                if constexpr (SHIFT) de = fmaf(rstd, ge - fmaf(xhe, c2, c1), MODE == kPlain ? 0.f : he_q[0]);
+                if constexpr (SHIFT) de = fmaf(rstd, ge - fmaf(xhe, c2, c1), MODE == kPlain ? 0.f : load1(he_q));
                 if constexpr (MODE != kPlain) {
                     if (dres) {
                         ch.store_row(dres, e, gg);

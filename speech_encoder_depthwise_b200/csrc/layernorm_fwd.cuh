@@ -70,15 +70,15 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     const float inv = 1.f / static_cast<float>(ch.C);
     int flip = 0;
     Oct<T> xo[NO], ro[NO];
-    float xe = 0.f, re = 0.f;
+    T xe = zero1<T>(), re = xe;  // as loaded: a conversion in `fetch` would wait for the load
     const auto fetch = [&](const RowWalk &w, bool any = false) {
         if (!w.in() || !(any || w.valid())) return;
         const int64_t e = ch.at(w.r);
         ch.load_row(x, e, xo);
         if (MODE != kPlain && res) ch.load_row(res, e, ro);
         if (ch.edge()) {
-            xe = load1(x + ch.edge_at(w.r));
-            if (MODE != kPlain && res) re = load1(res + ch.edge_at(w.r));
+            xe = x[ch.edge_at(w.r)];
+            if (MODE != kPlain && res) re = res[ch.edge_at(w.r)];
         }
     };
 #pragma unroll
@@ -102,7 +102,7 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         float ve = 0.f;
 #pragma unroll
         for (int j = 0; j < NO; ++j) xo[j].get(v[j]);
-        if constexpr (SHIFT) ve = xe;
+        if constexpr (SHIFT) ve = load1(&xe);
         if constexpr (MODE == kFusedDrop) {
             if constexpr (SHIFT) D.apply(static_cast<uint32_t>(e >> 3), TPR, v, ch.edge_at(r), ve);
             else D.apply(static_cast<uint32_t>(e >> 3), TPR, v);
@@ -119,7 +119,7 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
             for (int i = 0; i < 4; ++i) sum = fadd2(sum, v[j][i]);
         }
         if constexpr (SHIFT) {
-            if constexpr (MODE != kPlain) ve = fmaf(a.mult, ve, re);
+            if constexpr (MODE != kPlain) ve = fmaf(a.mult, ve, load1(&re));
             sum.x += ve;  // zero where the thread has no edge channel
         }
         w.next();

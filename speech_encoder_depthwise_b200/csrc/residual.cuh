@@ -34,6 +34,7 @@ struct SmemGrant {
 
 // One element of any type at any alignment, as float32 and back.
 template <typename T> __device__ __forceinline__ float load1(const T *p) { return static_cast<float>(*p); }
+template <typename T> __device__ __forceinline__ T zero1() { return static_cast<T>(0.f); }
 template <typename T> __device__ __forceinline__ void store1(T *p, float v) {
     const float2 f[1] = {make_float2(v, 0.f)};
     Vec<T, 1>::store(p, f);
