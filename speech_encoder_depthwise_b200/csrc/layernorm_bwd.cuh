@@ -42,6 +42,25 @@ template <int N> __device__ __forceinline__ void stage_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The same for one element e of a 16-bit tensor of n elements, by way of the aligned 4 bytes it lies in (cp.async
+// moves no fewer), or by itself where half of them lie outside the tensor.  Edges held in registers two
+// rows ahead instead made a row wait for their loads (dropout+add+ln 32x1500x1023 bf16 111 us, staged 95; 777
+// channels 104 / 87); float32 is faster with registers (32x1500x1023 104 us, staged 107).
+template <typename T> constexpr bool kStageEdges = sizeof(T) == 2;
+template <typename T> __device__ __forceinline__ int odd_half(const T *p) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) / 2 & 1);
+}
+template <typename T> __device__ __forceinline__ void stage_edge(uint32_t *dst, const T *t, int64_t e, int64_t n) {
+    const int half = odd_half(t + e);
+    if (e >= half && e - half + 2 <= n)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(t + e - half) : "memory");
+    else
+        reinterpret_cast<T *>(dst)[half] = t[e];
+}
+template <typename T> __device__ __forceinline__ float staged_edge(const uint32_t *src, const T *t, int64_t e) {
+    return load1(reinterpret_cast<const T *>(src) + odd_half(t + e));
+}
+
 // Thread-block clusters: all blocks arrived, and a float of another block's shared memory.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
@@ -95,6 +114,9 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
     Oct<T> *stage = reinterpret_cast<Oct<T> *>(smem) + threadIdx.x;
     constexpr int kTensorStep = NO * kThreads, kStageStep = kTensors * kTensorStep;
     float *sp = reinterpret_cast<float *>(smem + static_cast<size_t>(kStages) * kStageStep * sizeof(Oct<T>));
+    constexpr bool kEdgeStage = SHIFT && kStageEdges<T>;
+    uint32_t *edge_stage = reinterpret_cast<uint32_t *>(sp + 8 * Q) + threadIdx.x;  // [kStages][kTensors][kThreads]
+    const int64_t elements = static_cast<int64_t>(rows) * ch.C;
     float gamma_e = 0.f;
     grid_dependency_wait();
 
@@ -103,9 +125,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
     pipe.start(a.lengths, first, grid * GPB, rows, static_cast<int>(a.T));
     uint32_t valid = 0;  // bit i: row i from the one at hand is valid
     float mean_q[kStages] = {}, rstd_q[kStages] = {};
-    T xe_q[kStages], ge_q[kStages], he_q[kStages];  // as loaded: a conversion here would wait for the load
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) xe_q[i] = ge_q[i] = he_q[i] = zero1<T>();
+    float xe_q[kStages] = {}, ge_q[kStages] = {}, he_q[kStages] = {};
     // buf: stage; slot: place in the queues and in valid.  Nothing is staged for a masked row: its copies,
     // which nobody waits for, could land after the next ones into the same stage.
     const auto request = [&](int buf, int slot) {
@@ -123,10 +143,15 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
             }
             mean_q[slot] = a.mean[pipe.r];
             rstd_q[slot] = a.rstd[pipe.r];
-            if (ch.edge()) {
-                xe_q[slot] = x[ch.edge_at(pipe.r)];
-                ge_q[slot] = dy[ch.edge_at(pipe.r)];
-                if (MODE != kPlain && dh) he_q[slot] = dh[ch.edge_at(pipe.r)];
+            if (kEdgeStage && ch.edge()) {
+                uint32_t *se = edge_stage + buf * (kTensors * kThreads);
+                stage_edge(se, x, ch.edge_at(pipe.r), elements);
+                stage_edge(se + kThreads, dy, ch.edge_at(pipe.r), elements);
+                if (MODE != kPlain && dh) stage_edge(se + 2 * kThreads, dh, ch.edge_at(pipe.r), elements);
+            } else if (ch.edge()) {
+                xe_q[slot] = load1(x + ch.edge_at(pipe.r));
+                ge_q[slot] = load1(dy + ch.edge_at(pipe.r));
+                if (MODE != kPlain && dh) he_q[slot] = load1(dh + ch.edge_at(pipe.r));
             }
         }
         stage_commit();
@@ -207,12 +232,17 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
                 }
             }
             if constexpr (SHIFT) {
+                if (kEdgeStage && ch.edge() && live) {
+                    const uint32_t *se = edge_stage + buf * (kTensors * kThreads);
+                    xe_q[0] = staged_edge(se, x, ch.edge_at(r));
+                    ge_q[0] = staged_edge(se + kThreads, x, ch.edge_at(r));
+                    if (MODE != kPlain && dh) he_q[0] = staged_edge(se + 2 * kThreads, x, ch.edge_at(r));
+                }
                 if (ch.edge() && live) {
-                    const float dye = load1(ge_q);
-                    xhe = (load1(xe_q) - mean) * rstd;
-                    age = fmaf(dye, xhe, age);
-                    abe += dye;
-                    ge = dye * gamma_e;
+                    xhe = (xe_q[0] - mean) * rstd;
+                    age = fmaf(ge_q[0], xhe, age);
+                    abe += ge_q[0];
+                    ge = ge_q[0] * gamma_e;
                     s1.x += ge;
                     s2.x = fmaf(ge, xhe, s2.x);
                 }
@@ -238,7 +268,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
                     }
                 }
                 float de = 0.f;
-                if constexpr (SHIFT) de = fmaf(rstd, ge - fmaf(xhe, c2, c1), MODE == kPlain ? 0.f : load1(he_q));
+                if constexpr (SHIFT) de = fmaf(rstd, ge - fmaf(xhe, c2, c1), MODE == kPlain ? 0.f : he_q[0]);
                 if constexpr (MODE != kPlain) {
                     if (dres) {
                         ch.store_row(dres, e, gg);
@@ -264,9 +294,11 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
         for (int i = 0; i + 1 < kStages; ++i) {
             mean_q[i] = mean_q[i + 1];
             rstd_q[i] = rstd_q[i + 1];
-            xe_q[i] = xe_q[i + 1];
-            ge_q[i] = ge_q[i + 1];
-            he_q[i] = he_q[i + 1];
+            if constexpr (!kEdgeStage) {
+                xe_q[i] = xe_q[i + 1];
+                ge_q[i] = ge_q[i + 1];
+                he_q[i] = he_q[i + 1];
+            }
         }
         request(buf, kStages - 1);
         buf = buf + 1 == kStages ? 0 : buf + 1;
@@ -340,7 +372,8 @@ cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, SHIFT, MODE>;
     const size_t words = 8 * static_cast<size_t>(shifted_q(static_cast<int>(a.C)));
     const size_t stages = 2 * static_cast<size_t>(kTensors) * NO * kThreads * sizeof(Oct<T>);
-    const size_t during = stages + words * sizeof(float), after = (kUnits + 1) * 2 * words * sizeof(float);
+    const size_t edges = SHIFT && kStageEdges<T> ? 2 * kTensors * kThreads * sizeof(uint32_t) : 0;
+    const size_t during = stages + words * sizeof(float) + edges, after = (kUnits + 1) * 2 * words * sizeof(float);
     const size_t smem = during > after ? during : after;
     if (smem > 226 * 1024) return cudaErrorNotSupported;
     // a carve-out with room for a finalize block beside this one (519 float32 channels: 5.0 us for 148 rows
