@@ -12,21 +12,24 @@ enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual ad
 
 // Threads of a block, one block on an SM: as many as the registers of NO octets leave room for without
 // spills (dgamma, dbeta, xh and g: 32 registers an octet) and float32's staging area, a multiple of
-// 128 so that the four partitions of an SM hold the same number of warps, and of TPR.  `heavy`: edges and
-// the residual (dropout+add+ln 32x1500x1023 bf16 96 us with 256 threads, 105 with 384 and spills).
-template <typename T> constexpr int threads_for(int TPR, int NO, bool heavy) {
+// 128 so that the four partitions of an SM hold the same number of warps, and of TPR.  `heavy`: four octets
+// with the residual, where either edges are held too (dropout+add+ln 32x1500x1023 bf16 95 us with 256 threads,
+// 112 with 384 and spills) or no mask is drawn, so that memory is the bound and fewer rows at once suffice
+// (32x1500x2048 bf16 150 us with 256, 174 with 384; with dropout 163 and 156).
+constexpr bool heavy(bool SHIFT, int mode) { return mode == kFused || (SHIFT && mode == kFusedDrop); }
+template <typename T> constexpr int threads_for(int TPR, int NO, bool four256) {
     constexpr bool f32 = sizeof(T) == 4;
     const int most = NO == 1   ? 768
                      : NO == 2 ? 512
                      : NO == 3 ? (f32 && TPR > 32 ? 256 : 384)
-                               : (f32 || heavy ? 256 : 384);
+                               : (f32 || four256 ? 256 : 384);
     return most / TPR * TPR;
 }
 
 // Registers of a thread: what leaves room on every partition for one warp of 32 registers, so that the
 // finalize kernel's blocks wait on the same SMs and start at once (4.4 -> 1.6 us behind 1024 channels).
-template <typename T> constexpr int regs_for(int TPR, int NO, bool heavy) {
-    return (16384 - 1024) * 4 / threads_for<T>(TPR, NO, heavy) / 8 * 8;
+template <typename T> constexpr int regs_for(int TPR, int NO, bool four256) {
+    return (16384 - 1024) * 4 / threads_for<T>(TPR, NO, four256) / 8 * 8;
 }
 
 // A thread's own octets on their way from global to shared memory (cp.async): it waits for its own
@@ -89,9 +92,9 @@ constexpr int kCluster = 8;
 // small ones pay about 3 us for the two sums after the last row (block 1.2 us, finalize 1.6 us)
 // beside launch and first load.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
-__global__ void __maxnreg__(regs_for<T>(TPR, NO, SHIFT && MODE != kPlain))
+__global__ void __maxnreg__(regs_for<T>(TPR, NO, heavy(SHIFT, MODE)))
 layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
-    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR;
+    constexpr int kThreads = threads_for<T>(TPR, NO, heavy(SHIFT, MODE)), GPB = kThreads / TPR;
     constexpr int kTensors = MODE == kPlain ? 2 : 3, kStages = 2;
     constexpr int kUnits = TPR < 32 && !SHIFT ? kThreads / 32 : GPB;
     static_assert(TPR <= 32 || GPB <= 15, "a named barrier per group, numbers 1 to 15");
@@ -366,7 +369,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
 
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
-    constexpr int kThreads = threads_for<T>(TPR, NO, SHIFT && MODE != kPlain), GPB = kThreads / TPR;
+    constexpr int kThreads = threads_for<T>(TPR, NO, heavy(SHIFT, MODE)), GPB = kThreads / TPR;
     constexpr int kTensors = MODE == kPlain ? 2 : 3;
     constexpr int kUnits = TPR < 32 && !SHIFT ? kThreads / 32 : GPB;
     const auto kern = layernorm_bwd_rows_kernel<T, TPR, NO, SHIFT, MODE>;
