@@ -87,8 +87,8 @@ constexpr int kCluster = 8;
 // Bound by HBM for long batches; staged copies cost no registers, which dgamma and dbeta take (rows
 // of 2048 bf16, 32x1500: 84.5 us, 196 with a block of 256 loading one row at a time).  Measured (graph
 // replay, cold inputs, finalize included; fraction of the measured copy bandwidth): 32x1500x2048
-// bf16 84.5 us (0.89), with dropout and residual 32x1500x1024 bf16 76.9 us (0.83) and 16x1500x512
-// bf16 22.7 us (0.70), 16x1500x512 bf16 15.7 us (0.60), 8x733x519 float32 12.4 us (0.38).  The
+// bf16 84.5 us (0.89), with dropout and residual 32x1500x1024 bf16 75.9 us (0.84) and 16x1500x512
+// bf16 22.7 us (0.70), 16x1500x512 bf16 15.6 us (0.60), 8x733x519 float32 12.4 us (0.37).  The
 // small ones pay about 3 us for the two sums after the last row (block 1.2 us, finalize 1.6 us)
 // beside launch and first load.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>

@@ -30,7 +30,8 @@ enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual ad
 // Measured (graph replay, cold inputs; fraction of the measured copy bandwidth): 64x3000x1024 bf16
 // 111.6 us (0.94), 32x1500x1024 float32 56.6 us (0.93), 16x1500x512 bf16 10.0 us (0.66: about 3.5 us
 // of launch, first load and last store), 64 rows of 512 1.6 us; with dropout and residual 32x1500x1024
-// bf16 60.3 us (0.87), 16x1499x1023 fp16 36.6 us (0.72).
+// bf16 60.3 us (0.87), 16x1499x1023 fp16 34.3 us (0.76; 36.6 with edges converted
+// where they are loaded, which waits for them).
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(TPR, NO, sizeof(T)))
 layernorm_fwd_rows_kernel(const ResidualArgs a) {
