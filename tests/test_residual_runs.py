@@ -241,7 +241,7 @@ def test_every_row_kernel_with_several_rows_a_group(octets, rows, extra, dtype):
     run_dal_bwd(c, 0.2, 0.5)
 
 
-@pytest.mark.parametrize("C", [64, 512, 2048])
+@pytest.mark.parametrize("C", [64, 512, 2048, 8200])
 def test_parameters_off_their_boundary(C):
     """gamma and beta that start 4 bytes after a 32-byte boundary, and no gamma at all."""
     c = Case(3, 50, C, "bf16", lengths=[50, 20, 0], seed=C)
