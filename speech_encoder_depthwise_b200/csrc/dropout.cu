@@ -7,12 +7,16 @@
 namespace dwk {
 namespace {
 
+// x and res are read by ordinary loads, never as read-only data (no __restrict__, which would let the
+// compiler take that path): the previous kernel may write them while this one is already resident.  A
+// thread's loads come before its stores, which the compiler may no longer exchange.
+
 // A thread takes the 8 elements of one mask block, element by element.
 template <typename T>
 __global__ void __launch_bounds__(256)
-dropout_add_general_kernel(const T *__restrict__ x, const T *__restrict__ res, T *__restrict__ y,
-                           const int32_t *__restrict__ lengths, const unsigned long long *__restrict__ rng,
-                           uint32_t thr, float mult, int64_t B, int64_t Tn, int64_t C) {
+dropout_add_general_kernel(const T *x, const T *res, T *y, const int32_t *__restrict__ lengths,
+                           const unsigned long long *__restrict__ rng, uint32_t thr, float mult, int64_t B, int64_t Tn,
+                           int64_t C) {
     launch_dependents();
     grid_dependency_wait();
     DropoutRng R = {};
@@ -23,21 +27,31 @@ dropout_add_general_kernel(const T *__restrict__ x, const T *__restrict__ res, T
         const uint4 w4 = thr ? R.block(static_cast<uint64_t>(e0) >> 3) : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
         int64_t b = e0 / TC, i = e0 - b * TC, lim = clamp_len(lengths, b, Tn) * C;
+        T xv[8], rv[8];
+        unsigned in = 0;  // bit j: element j is valid
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int64_t e = e0 + j;
-            if (e >= N) break;
+            if (e0 + j >= N) break;
             if (i >= TC) {
                 i = 0;
                 lim = clamp_len(lengths, ++b, Tn) * C;
             }
-            float v = 0.f;
             if (i < lim) {
-                if (res) v = load1(res + e);
-                if (((w[j / 2] >> (16 * (j % 2))) & 0xffffu) >= thr) v = fmaf(mult, load1(x + e), v);
+                in |= 1u << j;
+                xv[j] = x[e0 + j];
+                if (res) rv[j] = res[e0 + j];
             }
-            store1(y + e, v);
             ++i;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (e0 + j >= N) break;
+            float v = 0.f;
+            if (in >> j & 1u) {
+                if (res) v = load1(&rv[j]);
+                if (((w[j / 2] >> (16 * (j % 2))) & 0xffffu) >= thr) v = fmaf(mult, load1(&xv[j]), v);
+            }
+            store1(y + e0 + j, v);
         }
     }
 }
@@ -54,9 +68,9 @@ dropout_add_general_kernel(const T *__restrict__ x, const T *__restrict__ res, T
 constexpr int kChunkOctets = 4;
 template <typename T, bool DROP, bool RES>
 __global__ void __launch_bounds__(256)
-dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *__restrict__ y,
-                         const int32_t *__restrict__ lengths, const unsigned long long *__restrict__ rng, uint32_t thr,
-                         float mult, int64_t B, int64_t Tn, int64_t C) {
+dropout_add_octet_kernel(const T *x, const T *res, T *y, const int32_t *__restrict__ lengths,
+                         const unsigned long long *__restrict__ rng, uint32_t thr, float mult, int64_t B, int64_t Tn,
+                         int64_t C) {
     constexpr int U = kChunkOctets, kStep = 256 * 8, kChunk = U * kStep;
     enum { kValid, kMasked, kMixed, kNone };
     launch_dependents();
@@ -138,6 +152,8 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
         if constexpr (DROP) D.apply(static_cast<uint32_t>(e0 >> 3), 0, keep);
         int64_t item = lengths ? item_of(e0) : 0, next = lengths ? (item + 1) * TC : N;
         int64_t lim = lengths ? item * TC + clamp_len(lengths, item, Tn) * C : N;
+        T xe[8], re[8];
+        unsigned in = 0;  // bit i: element i is valid
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t e = e0 + i;
@@ -146,12 +162,21 @@ dropout_add_octet_kernel(const T *__restrict__ x, const T *__restrict__ res, T *
                 lim = next + clamp_len(lengths, ++item, Tn) * C;
                 next += TC;
             }
-            float v = 0.f;
             if (e < lim) {
-                if constexpr (RES) v = load1(res + e);
-                if ((i % 2 ? keep[0][i / 2].y : keep[0][i / 2].x) != 0.f) v = fmaf(mult, load1(x + e), v);
+                in |= 1u << i;
+                xe[i] = x[e];
+                if constexpr (RES) re[i] = res[e];
             }
-            store1(y + e, v);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (e0 + i >= N) break;
+            float v = 0.f;
+            if (in >> i & 1u) {
+                if constexpr (RES) v = load1(&re[i]);
+                if ((i % 2 ? keep[0][i / 2].y : keep[0][i / 2].x) != 0.f) v = fmaf(mult, load1(&xe[i]), v);
+            }
+            store1(y + e0 + i, v);
         }
     }
 }
