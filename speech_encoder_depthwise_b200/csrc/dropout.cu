@@ -14,9 +14,8 @@ namespace {
 // A thread takes the 8 elements of one mask block, element by element.
 template <typename T>
 __global__ void __launch_bounds__(256)
-dropout_add_general_kernel(const T *x, const T *res, T *y, const int32_t *__restrict__ lengths,
-                           const unsigned long long *__restrict__ rng, uint32_t thr, float mult, int64_t B, int64_t Tn,
-                           int64_t C) {
+dropout_add_general_kernel(const T *x, const T *res, T *y, const int32_t *lengths, const unsigned long long *rng,
+                           uint32_t thr, float mult, int64_t B, int64_t Tn, int64_t C) {
     launch_dependents();
     grid_dependency_wait();
     DropoutRng R = {};
@@ -68,9 +67,8 @@ dropout_add_general_kernel(const T *x, const T *res, T *y, const int32_t *__rest
 constexpr int kChunkOctets = 4;
 template <typename T, bool DROP, bool RES>
 __global__ void __launch_bounds__(256)
-dropout_add_octet_kernel(const T *x, const T *res, T *y, const int32_t *__restrict__ lengths,
-                         const unsigned long long *__restrict__ rng, uint32_t thr, float mult, int64_t B, int64_t Tn,
-                         int64_t C) {
+dropout_add_octet_kernel(const T *x, const T *res, T *y, const int32_t *lengths, const unsigned long long *rng,
+                         uint32_t thr, float mult, int64_t B, int64_t Tn, int64_t C) {
     constexpr int U = kChunkOctets, kStep = 256 * 8, kChunk = U * kStep;
     enum { kValid, kMasked, kMixed, kNone };
     launch_dependents();

@@ -10,13 +10,15 @@
 
 #include <stdint.h>
 
+#include "dw_common.cuh"
+
 namespace dwk {
 
 struct DropoutRng {
     uint32_t k0, k1, o0, o1;  // key = seed, upper half of the counter = offset
 
     __device__ __forceinline__ void load(const unsigned long long *rng) {
-        const unsigned long long seed = __ldg(rng), offset = __ldg(rng + 1);
+        const unsigned long long seed = load_global(rng), offset = load_global(rng + 1);
         k0 = static_cast<uint32_t>(seed);
         k1 = static_cast<uint32_t>(seed >> 32);
         o0 = static_cast<uint32_t>(offset);

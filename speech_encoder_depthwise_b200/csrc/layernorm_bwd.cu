@@ -48,7 +48,7 @@ layernorm_bwd_general_kernel(const ResidualArgs a) {
         float2 acc = make_float2(0.f, 0.f);
         for (int64_t c = threadIdx.x; c < a.C; c += 256) {
             const float xh = (load1(x + base + c) - mean) * rstd, d = load1(dy + base + c);
-            const float g = a.gamma ? d * __ldg(a.gamma + c) : d;
+            const float g = a.gamma ? d * load_global(a.gamma + c) : d;
             acc.x += g;
             acc.y = fmaf(g, xh, acc.y);
             if (params) {
@@ -62,7 +62,7 @@ layernorm_bwd_general_kernel(const ResidualArgs a) {
         for (int64_t c = threadIdx.x; c < a.C; c += 256) {
             const int64_t e = base + c;
             const float xh = (load1(x + e) - mean) * rstd, d = load1(dy + e);
-            const float g = a.gamma ? d * __ldg(a.gamma + c) : d;
+            const float g = a.gamma ? d * load_global(a.gamma + c) : d;
             float ds = rstd * (g - c1 - xh * c2);
             if (dh) ds += load1(dh + e);
             if (dres) store1(dres + e, ds);
@@ -190,8 +190,7 @@ cudaError_t launch_wide(const ResidualArgs &a, int *G, cudaStream_t s) {
 // beside the row kernel's on an SM, so they are resident and waiting when it ends (and read the partial
 // rows, written meanwhile, from L2).
 __global__ void __launch_bounds__(128, 16)
-layernorm_bwd_finalize_kernel(const float *__restrict__ partials, float *__restrict__ dgamma,
-                              float *__restrict__ dbeta, int G, int64_t C) {
+layernorm_bwd_finalize_kernel(const float *partials, float *dgamma, float *dbeta, int G, int64_t C) {
     __shared__ float red[8][17];
     launch_dependents();
     const int lane = threadIdx.x % 16, q = threadIdx.x / 16;

@@ -167,7 +167,7 @@ layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
     constexpr bool kShared = SHIFT || TPR > 32;
     if constexpr (kShared) {
         for (int c = threadIdx.x; c < ch.C; c += kThreads)
-            sp[SHIFT ? shifted_at(c, Q) : halves_at(c, Q)] = a.gamma ? __ldg(a.gamma + c) : 1.f;
+            sp[SHIFT ? shifted_at(c, Q) : halves_at(c, Q)] = a.gamma ? load_global(a.gamma + c) : 1.f;
         __syncthreads();
         if (ch.edge()) gamma_e = sp[shifted_at(ch.ce, Q)];
     }

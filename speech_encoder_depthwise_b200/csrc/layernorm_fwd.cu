@@ -52,7 +52,7 @@ layernorm_fwd_general_kernel(const ResidualArgs a) {
         for (int64_t c = threadIdx.x; c < a.C; c += 256) {
             const float v = sum_at(c);
             if (h) store1(h + base + c, v);
-            const float ga = a.gamma ? __ldg(a.gamma + c) : 1.f, be = a.beta ? __ldg(a.beta + c) : 0.f;
+            const float ga = a.gamma ? load_global(a.gamma + c) : 1.f, be = a.beta ? load_global(a.beta + c) : 0.f;
             store1(y + base + c, fmaf((v - mean) * rstd, ga, be));
         }
         if (threadIdx.x == 0) {

@@ -60,7 +60,8 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     if constexpr (SHIFT) {
         const int Q = shifted_q(ch.C);
         for (int c = threadIdx.x; c < ch.C; c += kThreads)
-            sp[shifted_at(c, Q)] = make_float2(a.gamma ? __ldg(a.gamma + c) : 1.f, a.beta ? __ldg(a.beta + c) : 0.f);
+            sp[shifted_at(c, Q)] = make_float2(a.gamma ? load_global(a.gamma + c) : 1.f,
+                                               a.beta ? load_global(a.beta + c) : 0.f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) off[i] = shifted_at(ch.head + i, Q) + ch.lane;
         __syncthreads();
@@ -89,6 +90,11 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
     }
     // the next row is requested ahead where two rows fit 128 registers a thread
     constexpr bool kAhead = NO * sizeof(T) * (MODE == kPlain ? 1 : 2) <= 16;
+    // few rows of a 16-bit type behind a residual add: gamma and beta together with the row, since their loads can
+    // pass neither the sums' barriers nor the stores of h (600 rows of 1024 bf16 with dropout 2.95 us, behind them
+    // 3.07; 64 rows of 512 1.94 / 2.14).  float32 lacks the registers (16x1500x1024 60.6 / 59.6), and without h it
+    // gains nothing (1500 rows of 512 2.04 / 2.02)
+    constexpr bool kEarly = !SHIFT && MODE != kPlain && sizeof(T) == 2 && NO == 2 && TPR >= 32;
     RowWalk w;
     w.start(a.lengths, first, grid * GPB, rows, static_cast<int>(a.T));
     if (kAhead) fetch(w, true);  // whatever its length says: the two loads' latencies overlap
@@ -101,6 +107,16 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         const int64_t e = ch.at(r);
         float2 v[NO][4], sum = make_float2(0.f, 0.f);
         float ve = 0.f;
+        float2 ga[NO][4], be[NO][4];
+        const auto params = [&](int j) {
+            load_params8(a.gamma + ch.c0(j), ga[j]);
+            load_params8(a.beta + ch.c0(j), be[j]);
+        };
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int j = 0; j < NO; ++j)
+                if (ch.any(j)) params(j);
+        }
 #pragma unroll
         for (int j = 0; j < NO; ++j) xo[j].get(v[j]);
         if constexpr (SHIFT) ve = load1(&xe);
@@ -165,14 +181,12 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
                     v[j][i] = make_float2(fmaf(t.x, p.x, p.y), fmaf(t.y, q.x, q.y));
                 }
             } else {
-                float2 ga[4], be[4];
-                load_params8(a.gamma + ch.c0(j), ga);
-                load_params8(a.beta + ch.c0(j), be);
+                if constexpr (!kEarly) params(j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[j][i] = ffma2(fmul2(v[j][i], both(rstd)), ga[i], be[i]);
+                for (int i = 0; i < 4; ++i) v[j][i] = ffma2(fmul2(v[j][i], both(rstd)), ga[j][i], be[j][i]);
             }
-            Oct<T>::store(y + e + 8 * j * TPR, v[j]);
         }
+        ch.store_row(y, e, v);  // behind every octet's gamma and beta, whose loads cannot pass a store
         if (ch.edge()) store1(y + ch.edge_at(r), fmaf(ve * rstd, pe.x, pe.y));
         if (ch.lane == 0) {
             if (a.mean) a.mean[r] = mean;

@@ -1,4 +1,6 @@
 // Device helpers shared by the residual-path kernels (layer norm, dropout with the residual add).
+// Everything they read, parameters, lengths and generator state included, goes by ordinary loads: the previous
+// kernel in the stream may write it while this one is already resident, so none of it is read-only data.
 #pragma once
 
 #include <atomic>
@@ -46,8 +48,7 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Eight consecutive elements, moved with one instruction (16 bytes of a 16-bit type, 32 of float32):
 // the unit of the row kernels, and one block of the dropout generator.  Loads do not allocate in
-// L1 (every activation is read once), which leaves it to gamma and beta, nor take the read-only path:
-// the previous kernel in the stream may write them while this one is already resident.
+// L1 (every activation is read once), which leaves it to gamma and beta.
 template <typename T> struct Oct {
     using H = Half16<T>;
     uint4 r;
@@ -96,7 +97,7 @@ template <> struct Oct<float> {
 
 // Eight float32 parameters (32-byte aligned), kept in L1 for the rows to come.
 __device__ __forceinline__ void load_params8(const float *p, float2 (&f)[4]) {
-    asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y), "=f"(f[2].x), "=f"(f[2].y), "=f"(f[3].x),
                    "=f"(f[3].y)
                  : "l"(p) : "memory");
@@ -110,7 +111,7 @@ __device__ __forceinline__ void any_params8(const float *p, float missing, int64
         load_params8(p + c, f);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = make_float2(__ldg(p + c + 2 * i), __ldg(p + c + 2 * i + 1));
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(load_global(p + c + 2 * i), load_global(p + c + 2 * i + 1));
     }
 }
 
@@ -206,7 +207,7 @@ struct RowWalk {
             t = first - b * T;
             db = static_cast<int>(static_cast<uint32_t>(step) / static_cast<uint32_t>(T));
             dt = step - db * T;
-            if (in()) len = __ldg(lengths + b);
+            if (in()) len = load_global(lengths + b);
         }
     }
     __device__ __forceinline__ bool in() const { return r < rows; }
@@ -220,7 +221,7 @@ struct RowWalk {
                 t -= T;
                 ++b;
             }
-            if (in()) len = __ldg(lengths + b);
+            if (in()) len = load_global(lengths + b);
         }
     }
 };

@@ -10,7 +10,7 @@ import pytest
 
 from speech_encoder_depthwise_b200 import build
 
-RESTRICT = r"const\s+[\w ]+\*\s*__restrict__\s*(\w+)"
+READ_ONLY = r"__ldg\s*\(|\bld\.global[\w.:]*\.nc\b|const\s+[\w ]+\*\s*__restrict__"
 
 
 def code(name):
@@ -19,7 +19,23 @@ def code(name):
         return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
 
 
-@pytest.mark.parametrize("name", ["dropout.cu"])
-def test_no_activation_is_declared_read_only(name):
-    params = re.findall(RESTRICT, code(name))
-    assert not [p for p in params if p in ("x", "res")]
+def function(text, name):
+    """The body of the first function of that name."""
+    at = text.index("{", text.index(name + "("))
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i + 1]
+
+
+@pytest.mark.parametrize("name", ["dropout.cu", "dropout.cuh", "residual.cuh", "layernorm_fwd.cu", "layernorm_fwd.cuh",
+                                  "layernorm_bwd.cu", "layernorm_bwd.cuh"])
+def test_residual_path_reads_nothing_as_read_only(name):
+    """Activations, parameters, lengths, generator state and partial rows."""
+    assert re.findall(READ_ONLY, code(name)) == []
+
+
+def test_lengths_are_not_read_as_read_only():
+    """An earlier call may write them: dw_subsample_fwd and dwconv2d_fwd do (out_lengths)."""
+    assert re.findall(READ_ONLY, function(code("dw_common.cuh"), "clamp_len")) == []

@@ -73,3 +73,44 @@ def test_dropout_reads_what_the_call_before_wrote(lens, T, C, offset, dtype):
             dw.dw_dropout_add_bwd(z[i], h, rng[i], 0.125, 0.5, ln)
             after()
     check_graph(run, z, [(h, src)])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,C", [(40, 512), (40, 519), (600, 64), (9, 2048), (5, 8200), (5, 8201)])
+def test_parameters_and_lengths_that_the_call_before_wrote(T, C, dtype):
+    """gamma, beta, the generator's state and the lengths of a call are what the call before it (dgamma and dbeta, the
+    out_lengths of a subsampler) or a copy between two calls wrote over other values."""
+    B, steps, F = 3, 20, 8
+    torch.manual_seed(C + T)
+    x, dy = (torch.randn(B, T, C, device="cuda").to(dtype) for _ in range(2))
+    mel = torch.randn(B, 4 * T, F, device="cuda")
+    w = [torch.randn(s, device="cuda") for s in ((3, 3, 8), (8,), (3, 3, 8), (8,))]
+    sub = torch.empty((B,) + dw.subsample_out_shape(4 * T, F) + (8,), device="cuda")
+    assert sub.shape[1] == T
+    frames = torch.randint(0, 4 * T + 1, (steps, B), dtype=torch.int32, device="cuda")
+    frames[:, 0] = 4 * T
+    rngs = torch.stack([torch.full((steps,), 7), torch.arange(steps)], 1).cuda()
+    m, r = x.float().mean(-1), torch.rsqrt(x.float().var(-1, unbiased=False) + EPS)
+    ln, rng = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda")
+    dx, h = torch.empty_like(x), torch.empty_like(x)
+    ga, be = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    ws = torch.empty(dw.dw_layernorm_bwd_workspace_size(B, T, C), dtype=torch.uint8, device="cuda")
+    y, z = (torch.empty(steps, B, T, C, dtype=dtype, device="cuda") for _ in range(2))
+    gamma, beta = torch.rand(C, device="cuda"), torch.rand(C, device="cuda")
+
+    def run(after):
+        for i in range(steps):
+            rng.copy_(rngs[i])
+            dw.dw_dropout_add_layernorm_fwd(x, None, rng, 0.25, 1.0, ga, be, h, z[i], None, None, ln, EPS)
+            after()
+            dw.dw_subsample_fwd(mel, *w, sub, frames[i], ln, False)
+            after()
+            dw.dw_layernorm_bwd(h, dy, None, m, r, dx, ga, be, ln, ws)
+            after()
+            dw.dw_layernorm_fwd(x, ga, be, y[i], None, None, ln, EPS)
+            after()
+            dw.dw_subsample_fwd(mel, *w, sub, frames[steps - 1 - i], ln, False)
+            after()
+            dw.dw_dropout_add_fwd(y[i], x, h, rng, 0.5, 1.0, ln)
+            after()
+    check_graph(run, [y, z], [(ga, gamma), (be, beta), (ln, torch.full_like(ln, T)), (h, x), (dx, x)])
