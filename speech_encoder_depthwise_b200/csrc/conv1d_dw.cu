@@ -35,10 +35,8 @@ constexpr int kDwMaxRows16 = 16; // partial rows of the register-tiled kernel
 
 template <typename T, int V, int KB, int R>
 __global__ void __cluster_dims__(kDwCluster, 1, 1) __launch_bounds__(kDwThreads, 2)
-conv1d_dw_partial_kernel(const T *__restrict__ x, const T *__restrict__ dy,
-                         const int32_t *__restrict__ lengths, float *__restrict__ partials,
-                         int64_t B, int64_t Tn, int C, int K, int k_off, int pad_left, int TX,
-                         int nTC, int with_bias) {
+conv1d_dw_partial_kernel(const T *x, const T *dy, const int32_t *lengths, float *__restrict__ partials, int64_t B,
+                         int64_t Tn, int C, int K, int k_off, int pad_left, int TX, int nTC, int with_bias) {
     extern __shared__ float smem[];  // [TY][KB+1][CT]
     constexpr int NP = Pairs<V>::n;
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
@@ -212,9 +210,8 @@ struct DwTmaShape {
 template <typename T, int V, int KB, bool FUSED = false>
 __global__ void __launch_bounds__(DwTmaShape<T, V, KB, FUSED>::THREADS, FUSED ? 1 : kDwBlocks)
 conv1d_dw_tma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
-                     const int32_t *__restrict__ lengths, float *__restrict__ partials, int B, int Tn, int C, int K,
-                     int k_off, int pad_left, int nT, int with_bias, int ordered, const float *__restrict__ wgt,
-                     T *__restrict__ dx) {
+                     const int32_t *lengths, float *__restrict__ partials, int B, int Tn, int C, int K, int k_off,
+                     int pad_left, int nT, int with_bias, int ordered, const float *wgt, T *__restrict__ dx) {
     using S = DwTmaShape<T, V, KB, FUSED>;
     const int padR = K - 1 - pad_left;  // the data gradient's left pad
     constexpr int NP = Pairs<V>::n;
@@ -500,9 +497,8 @@ struct DwSpanShape {
 template <typename T, int V, int KB, bool PACKED, bool FUSED = false>
 __global__ void __launch_bounds__(DwSpanShape<T, V, KB, FUSED>::THREADS, FUSED ? 1 : kDwBlocks)
 conv1d_dw_span_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
-                      const int32_t *__restrict__ lengths, float *__restrict__ partials, int B, int Tn, int C,
-                      int K, int k_off, int pad_left, int with_bias, const float *__restrict__ wgt,
-                      T *__restrict__ dx) {
+                      const int32_t *lengths, float *__restrict__ partials, int B, int Tn, int C, int K, int k_off,
+                      int pad_left, int with_bias, const float *wgt, T *__restrict__ dx) {
     static_assert(!(PACKED && FUSED), "the one-pass backward takes padded batches");
     using S = DwSpanShape<T, V, KB, FUSED>;
     const int padR = K - 1 - pad_left;  // the data gradient's left pad
@@ -539,8 +535,8 @@ conv1d_dw_span_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
     for (int bb = static_cast<int>(threadIdx.x); bb < B; bb += static_cast<int>(blockDim.x)) {
         int s0 = 0, L;
         if constexpr (PACKED) {
-            s0 = __ldg(lengths + bb);
-            int e = __ldg(lengths + bb + 1);
+            s0 = load_global(lengths + bb);
+            int e = load_global(lengths + bb + 1);
             s0 = s0 < 0 ? 0 : (s0 > Tn ? Tn : s0);
             e = e < s0 ? s0 : (e > Tn ? Tn : e);
             L = e - s0;
@@ -787,8 +783,8 @@ conv1d_dw_span_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_con
 // with 8 row groups: group r adds rows r, r+8, r+16, ... in order, then the 8 group sums are
 // added in a fixed tree.  The order depends only on the row count, so results are reproducible.
 __global__ void __launch_bounds__(256)
-conv1d_dw_finalize_kernel(const float *__restrict__ partials, float *__restrict__ dw,
-                          float *__restrict__ dbias, int Gp, int K, int64_t C) {
+conv1d_dw_finalize_kernel(const float *partials, float *__restrict__ dw, float *__restrict__ dbias, int Gp, int K,
+                          int64_t C) {
     __shared__ float red[8][33];
     launch_dependents();     // the next kernel may start its own set-up
     grid_dependency_wait();  // launched programmatically after the partial kernel
@@ -798,7 +794,7 @@ conv1d_dw_finalize_kernel(const float *__restrict__ partials, float *__restrict_
     float s = 0.f;
     if (e < E) {
 #pragma unroll 4
-        for (int g = rg; g < Gp; g += 8) s += __ldg(partials + static_cast<int64_t>(g) * E + e);
+        for (int g = rg; g < Gp; g += 8) s += load_global(partials + static_cast<int64_t>(g) * E + e);
     }
     red[rg][col] = s;
     __syncthreads();
@@ -817,8 +813,8 @@ conv1d_dw_finalize_kernel(const float *__restrict__ partials, float *__restrict_
 // sums are added in a fixed tree.  Reproducible for a given row count.
 constexpr int kFinGroups = 16;
 __global__ void __launch_bounds__(256)
-conv1d_dw_finalize4_kernel(const float *__restrict__ partials, float *__restrict__ dw,
-                           float *__restrict__ dbias, int Gp, int K, int64_t C) {
+conv1d_dw_finalize4_kernel(const float *partials, float *__restrict__ dw, float *__restrict__ dbias, int Gp, int K,
+                           int64_t C) {
     __shared__ float4 red[kFinGroups][16];
     launch_dependents();     // the next kernel may start its own set-up
     grid_dependency_wait();  // launched programmatically after the partial kernel
@@ -832,7 +828,7 @@ conv1d_dw_finalize4_kernel(const float *__restrict__ partials, float *__restrict
 #pragma unroll
         for (int i = 0; i < kDwMaxRows / kFinGroups; ++i) {
             const int g = rg + i * kFinGroups;
-            v[i] = g < Gp ? __ldg(p4 + static_cast<int64_t>(g) * E4 + e4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = g < Gp ? load_global(p4 + static_cast<int64_t>(g) * E4 + e4) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int i = 0; i < kDwMaxRows / kFinGroups; ++i) {
@@ -1237,9 +1233,8 @@ constexpr int kDwPackedTaps = 16;
 
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
-conv1d_dw_packed_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int32_t *__restrict__ offsets,
-                        float *__restrict__ partials, int B, int N, int C, int K, int k_off, int kb, int pad_left,
-                        int with_bias, int G) {
+conv1d_dw_packed_kernel(const T *x, const T *dy, const int32_t *offsets, float *__restrict__ partials, int B, int N,
+                        int C, int K, int k_off, int kb, int pad_left, int with_bias, int G) {
     constexpr int NP = Pairs<V>::n;
     constexpr int KT = kDwPackedTaps;
     extern __shared__ float red[];  // [8][KT + 1][32 V]
@@ -1248,7 +1243,7 @@ conv1d_dw_packed_kernel(const T *__restrict__ x, const T *__restrict__ dy, const
     const int cl = lane * V, c = blockIdx.y * CT + cl;
     const bool act = c < C;
     auto off = [&](int b) {
-        const int o = __ldg(offsets + b);
+        const int o = load_global(offsets + b);
         return o < 0 ? 0 : (o > N ? N : o);
     };
     const int64_t g = blockIdx.x;

@@ -31,10 +31,8 @@ namespace dwk {
 
 template <typename T, int V, int K, int R>
 __global__ void __launch_bounds__(256, 2)
-conv1d_fwd_vec_kernel(const T *__restrict__ x, const float *__restrict__ w,
-                      const float *__restrict__ bias, T *__restrict__ y,
-                      const int32_t *__restrict__ lengths, int64_t Tn, int C, int pad_left,
-                      int flip, int TX, int nT, int nC, int64_t units) {
+conv1d_fwd_vec_kernel(const T *x, const float *w, const float *bias, T *__restrict__ y, const int32_t *lengths,
+                      int64_t Tn, int C, int pad_left, int flip, int TX, int nT, int nC, int64_t units) {
     constexpr int NP = Pairs<V>::n;
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     const int TY = blockDim.x / TX;
@@ -176,9 +174,9 @@ struct TmaShape {
 // neighbouring items inside a tile are masked like frames past a length.
 template <typename T, int V, int K, bool PACKED = false>
 __global__ void __launch_bounds__(kTmaThreads, kTmaBlocks)
-conv1d_fwd_tma_kernel(const __grid_constant__ CUtensorMap xmap, const float *__restrict__ w,
-                      const float *__restrict__ bias, T *__restrict__ y, const int32_t *__restrict__ lengths,
-                      int B, int Tn, int C, int pad_left, int flip, int nT, int nC, int ntiles) {
+conv1d_fwd_tma_kernel(const __grid_constant__ CUtensorMap xmap, const float *w, const float *bias, T *__restrict__ y,
+                      const int32_t *lengths, int B, int Tn, int C, int pad_left, int flip, int nT, int nC,
+                      int ntiles) {
     using S = TmaShape<T, V, K>;
     constexpr int NP = Pairs<V>::n;
     constexpr int R = S::R;
@@ -229,7 +227,7 @@ conv1d_fwd_tma_kernel(const __grid_constant__ CUtensorMap xmap, const float *__r
                 const int bb = base + lane;
                 int nv = 0;
                 if (bb < B) {
-                    int s0 = __ldg(lengths + bb), e = __ldg(lengths + bb + 1);
+                    int s0 = load_global(lengths + bb), e = load_global(lengths + bb + 1);
                     s0 = s0 < 0 ? 0 : (s0 > Tn ? Tn : s0);
                     e = e < s0 ? s0 : (e > Tn ? Tn : e);
                     pst[bb] = s0;
@@ -385,10 +383,8 @@ conv1d_fwd_tma_kernel(const __grid_constant__ CUtensorMap xmap, const float *__r
 // (served from L1).  The general fallback for widths without a specialisation.
 template <typename T, int V, int R>
 __global__ void __launch_bounds__(256)
-conv1d_fwd_vec_anyk_kernel(const T *__restrict__ x, const float *__restrict__ w,
-                           const float *__restrict__ bias, T *__restrict__ y,
-                           const int32_t *__restrict__ lengths, int64_t Tn, int64_t C, int K,
-                           int pad_left, int flip, int TX, int nT, int nC) {
+conv1d_fwd_vec_anyk_kernel(const T *x, const float *w, const float *bias, T *__restrict__ y, const int32_t *lengths,
+                           int64_t Tn, int64_t C, int K, int pad_left, int flip, int TX, int nT, int nC) {
     constexpr int NP = Pairs<V>::n;
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     const int TY = blockDim.x / TX;
@@ -510,15 +506,14 @@ cudaError_t launch_vec_anyk(const Conv1dArgs &a, cudaStream_t s) {
 // that no item covers are left unchanged.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
-conv1d_fwd_packed_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
-                         T *__restrict__ y, const int32_t *__restrict__ offsets, int B, int N, int C, int K,
-                         int pad_left, int flip, int nCV) {
+conv1d_fwd_packed_kernel(const T *x, const float *w, const float *bias, T *__restrict__ y, const int32_t *offsets,
+                         int B, int N, int C, int K, int pad_left, int flip, int nCV) {
     constexpr int NP = Pairs<V>::n;
     const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (idx >= static_cast<int64_t>(N) * nCV) return;
     const int n = static_cast<int>(idx / nCV), c = static_cast<int>(idx % nCV) * V;
     auto off = [&](int b) {
-        const int o = __ldg(offsets + b);
+        const int o = load_global(offsets + b);
         return o < 0 ? 0 : (o > N ? N : o);
     };
     int lo = 0, hi = B;  // the last item b with off(b) <= n

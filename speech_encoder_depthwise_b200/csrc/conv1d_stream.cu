@@ -59,9 +59,8 @@ __device__ __forceinline__ bool stream_idx(int B, int Tn, int nCV, int V, int S,
 // Compile-time K: the window win[0..K-1] holds xcat frames t .. t+K-1 of this thread's channels.
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kStreamThreads)
-conv1d_stream_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
-                     T *__restrict__ y, T *cache, const int32_t *__restrict__ lengths, int B, int Tn, int C,
-                     int nCV, int S, int nSeg) {
+conv1d_stream_kernel(const T *x, const float *w, const float *bias, T *__restrict__ y, T *cache, const int32_t *lengths,
+                     int B, int Tn, int C, int nCV, int S, int nSeg) {
     constexpr int H = K - 1;
     constexpr int P = Pairs<V>::n;
     launch_dependents();     // the next chunk's kernel may start its own set-up
@@ -131,9 +130,8 @@ conv1d_stream_kernel(const T *__restrict__ x, const float *__restrict__ w, const
 // Any K: the window is read from global memory (cache frames, then the chunk's valid frames).
 template <typename T, int V>
 __global__ void __launch_bounds__(kStreamThreads)
-conv1d_stream_anyk_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
-                          T *__restrict__ y, T *cache, const int32_t *__restrict__ lengths, int B, int Tn, int C,
-                          int K, int nCV, int S, int nSeg) {
+conv1d_stream_anyk_kernel(const T *x, const float *w, const float *bias, T *__restrict__ y, T *cache,
+                          const int32_t *lengths, int B, int Tn, int C, int K, int nCV, int S, int nSeg) {
     constexpr int P = Pairs<V>::n;
     const int H = K - 1;
     launch_dependents();     // the next chunk's kernel may start its own set-up

@@ -36,10 +36,9 @@ __device__ __forceinline__ void ld_frame(const T *p, float2 (&f)[Pairs<V>::n]) {
 // KTC/KFC > 0: a compiled window (taps in registers); 0: runtime KT, KF.
 template <typename T, int V, int KTC, int KFC>
 __global__ void __launch_bounds__(kC2Threads)
-dwconv2d_fwd_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
-                    T *__restrict__ y, const int32_t *__restrict__ lengths, int32_t *__restrict__ out_lengths, int B,
-                    int Tn, int F, int C, int KTr, int KFr, int st, int sf, int pt, int pb, int pf, int To, int Fo,
-                    int nCV) {
+dwconv2d_fwd_kernel(const T *x, const float *w, const float *bias, T *__restrict__ y, const int32_t *lengths,
+                    int32_t *__restrict__ out_lengths, int B, int Tn, int F, int C, int KTr, int KFr, int st, int sf,
+                    int pt, int pb, int pf, int To, int Fo, int nCV) {
     constexpr int P = Pairs<V>::n;
     const int KT = KTC > 0 ? KTC : KTr, KF = KFC > 0 ? KFC : KFr;
     const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -102,9 +101,8 @@ dwconv2d_fwd_kernel(const T *__restrict__ x, const float *__restrict__ w, const 
 // tap (p, q) lands on it.
 template <typename T, int V, int KTC, int KFC>
 __global__ void __launch_bounds__(kC2Threads)
-dwconv2d_dx_kernel(const T *__restrict__ dy, const float *__restrict__ w, T *__restrict__ dx,
-                   const int32_t *__restrict__ lengths, int B, int Tn, int F, int C, int KTr, int KFr, int st, int sf,
-                   int pt, int pb, int pf, int To, int Fo, int nCV) {
+dwconv2d_dx_kernel(const T *dy, const float *w, T *__restrict__ dx, const int32_t *lengths, int B, int Tn, int F, int C,
+                   int KTr, int KFr, int st, int sf, int pt, int pb, int pf, int To, int Fo, int nCV) {
     constexpr int P = Pairs<V>::n;
     const int KT = KTC > 0 ? KTC : KTr, KF = KFC > 0 ? KFC : KFr;
     const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -164,9 +162,9 @@ dwconv2d_dx_kernel(const T *__restrict__ dy, const float *__restrict__ w, T *__r
 // 0 .. KT*KF-1 the taps and KT*KF the bias.
 template <typename T, bool VEC2>
 __global__ void __launch_bounds__(kC2Threads)
-dwconv2d_dw_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int32_t *__restrict__ lengths,
-                   float *__restrict__ partials, int B, int Tn, int F, int C, int KT, int KF, int st, int sf, int pt,
-                   int pb, int pf, int To, int Fo, int nCG, int tap0, int with_bias) {
+dwconv2d_dw_kernel(const T *x, const T *dy, const int32_t *lengths, float *__restrict__ partials, int B, int Tn, int F,
+                   int C, int KT, int KF, int st, int sf, int pt, int pb, int pf, int To, int Fo, int nCG, int tap0,
+                   int with_bias) {
     const int cgp = blockIdx.x % nCG, g = blockIdx.x / nCG, G = gridDim.x / nCG;
     const int c = (cgp * kC2Threads + threadIdx.x) * 2;
     if (c >= C) return;
@@ -237,7 +235,7 @@ dwconv2d_dw_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int3
 
 // dW / dbias = the partial rows summed in a fixed order (8 row groups, then a fixed tree).
 __global__ void __launch_bounds__(256)
-dwconv2d_dw_finalize_kernel(const float *__restrict__ partials, int G, int ntap, int C, float *__restrict__ dw,
+dwconv2d_dw_finalize_kernel(const float *partials, int G, int ntap, int C, float *__restrict__ dw,
                             float *__restrict__ dbias) {
     __shared__ float red[8][33];
     const int col = threadIdx.x % 32, rg = threadIdx.x / 32;
@@ -245,7 +243,7 @@ dwconv2d_dw_finalize_kernel(const float *__restrict__ partials, int G, int ntap,
     const int64_t e = static_cast<int64_t>(blockIdx.x) * 32 + col;
     float s = 0.f;
     if (e < E)
-        for (int r = rg; r < G; r += 8) s += __ldg(partials + static_cast<int64_t>(r) * E + e);
+        for (int r = rg; r < G; r += 8) s += load_global(partials + static_cast<int64_t>(r) * E + e);
     red[rg][col] = s;
     __syncthreads();
     if (rg == 0 && e < E) {
@@ -257,8 +255,8 @@ dwconv2d_dw_finalize_kernel(const float *__restrict__ partials, int G, int ntap,
     }
 }
 
-__global__ void dwconv2d_out_lengths_kernel(const int32_t *__restrict__ lengths, int32_t *__restrict__ out_lengths,
-                                            int B, int Tn, int KT, int st, int pt, int pb, int To) {
+__global__ void dwconv2d_out_lengths_kernel(const int32_t *lengths, int32_t *__restrict__ out_lengths, int B, int Tn,
+                                            int KT, int st, int pt, int pb, int To) {
     const int b = blockIdx.x * blockDim.x + threadIdx.x;
     if (b >= B) return;
     const int Lo = conv_len(static_cast<int>(clamp_len(lengths, b, Tn)), pt, pb, KT, st);

@@ -110,9 +110,8 @@ __device__ __forceinline__ C2Smem c2_smem(unsigned char *raw, int stage_bytes) {
 // walks the TI rows; blockDim = TJ * CS/4 rounded up to a warp.
 template <typename T, int ST>
 __global__ void __launch_bounds__(512)
-c2_fwd_tma_kernel(const __grid_constant__ CUtensorMap xmap, const float *__restrict__ w,
-                  const float *__restrict__ bias, T *__restrict__ y, const int32_t *__restrict__ lengths,
-                  int32_t *__restrict__ out_lengths, C2Geo g) {
+c2_fwd_tma_kernel(const __grid_constant__ CUtensorMap xmap, const float *w, const float *bias, T *__restrict__ y,
+                  const int32_t *lengths, int32_t *__restrict__ out_lengths, C2Geo g) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const C2Smem sm = c2_smem(smem_raw, g.stage_bytes);
     const int tid = threadIdx.x;
@@ -274,8 +273,8 @@ c2_fwd_tma_kernel(const __grid_constant__ CUtensorMap xmap, const float *__restr
 // the box row of its dy term or -1; each thread's column gives the same for q.
 template <typename T>
 __global__ void __launch_bounds__(512)
-c2_dx_tma_kernel(const __grid_constant__ CUtensorMap gmap, const float *__restrict__ w, T *__restrict__ dx,
-                 const int32_t *__restrict__ lengths, C2Geo g) {
+c2_dx_tma_kernel(const __grid_constant__ CUtensorMap gmap, const float *w, T *__restrict__ dx, const int32_t *lengths,
+                 C2Geo g) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const C2Smem sm = c2_smem(smem_raw, g.stage_bytes);
     int *rowtab = reinterpret_cast<int *>(sm.stage[1] + g.stage_bytes);  // [TI][3]
@@ -416,8 +415,8 @@ __host__ __device__ constexpr int ph_tap(bool odd, int r, int e) { return ph_n(o
 
 template <typename T, bool RODD, bool CODD>
 __global__ void __launch_bounds__(512)
-c2_dx2_tma_kernel(const __grid_constant__ CUtensorMap gmap, const float *__restrict__ w, T *__restrict__ dx,
-                  const int32_t *__restrict__ lengths, C2Geo g) {
+c2_dx2_tma_kernel(const __grid_constant__ CUtensorMap gmap, const float *w, T *__restrict__ dx, const int32_t *lengths,
+                  C2Geo g) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const C2Smem sm = c2_smem(smem_raw, g.stage_bytes);
     const int tid = threadIdx.x;
@@ -569,7 +568,7 @@ c2_dx2_tma_kernel(const __grid_constant__ CUtensorMap gmap, const float *__restr
 template <typename T, int ST>
 __global__ void __launch_bounds__(512)
 c2_dw_tma_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap gmap,
-                 const int32_t *__restrict__ lengths, float *__restrict__ partials, C2Geo g, int G, int xbytes) {
+                 const int32_t *lengths, float *__restrict__ partials, C2Geo g, int G, int xbytes) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const C2Smem sm = c2_smem(smem_raw, g.stage_bytes);
     const int tid = threadIdx.x;

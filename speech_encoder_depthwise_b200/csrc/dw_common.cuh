@@ -26,21 +26,22 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // are resident: __ldg would let the compiler read it before grid_dependency_wait, or from a stale line.  The
 // address space is stated, because a load that might be of shared memory cannot be moved past a store there
 // (conv2d forward 16x750x20x256 bf16 30.7 us, with plain C++ loads of the lengths 31.4).
-__device__ __forceinline__ float load_global(const float *p) {
-    float v;
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ int32_t load_global(const int32_t *p) {
-    int32_t v;
-    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ unsigned long long load_global(const unsigned long long *p) {
-    unsigned long long v;
-    asm volatile("ld.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
-}
+#define DW_LOAD_GLOBAL(T, INSTRUCTION, ...)                                         \
+    __device__ __forceinline__ T load_global(const T *p) {                          \
+        T v;                                                                        \
+        asm volatile("ld.global." INSTRUCTION : __VA_ARGS__ : "l"(p) : "memory");   \
+        return v;                                                                   \
+    }
+DW_LOAD_GLOBAL(unsigned short, "u16 %0, [%1];", "=h"(v))
+DW_LOAD_GLOBAL(uint32_t, "u32 %0, [%1];", "=r"(v))
+DW_LOAD_GLOBAL(int32_t, "s32 %0, [%1];", "=r"(v))
+DW_LOAD_GLOBAL(unsigned long long, "u64 %0, [%1];", "=l"(v))
+DW_LOAD_GLOBAL(float, "f32 %0, [%1];", "=f"(v))
+DW_LOAD_GLOBAL(float2, "v2.f32 {%0, %1}, [%2];", "=f"(v.x), "=f"(v.y))
+DW_LOAD_GLOBAL(uint2, "v2.u32 {%0, %1}, [%2];", "=r"(v.x), "=r"(v.y))
+DW_LOAD_GLOBAL(float4, "v4.f32 {%0, %1, %2, %3}, [%4];", "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w))
+DW_LOAD_GLOBAL(uint4, "v4.u32 {%0, %1, %2, %3}, [%4];", "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w))
+#undef DW_LOAD_GLOBAL
 
 #ifdef DW_SCALAR_FMA
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
@@ -82,7 +83,7 @@ template <> struct Half16<f16> {
 template <typename T> struct Vec16x8 {
     using H = Half16<T>;
     uint4 r;
-    __device__ __forceinline__ void load(const T *p) { r = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load(const T *p) { r = load_global(reinterpret_cast<const uint4 *>(p)); }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void to_f2(float2 (&f)[4]) const {
         f[0] = H::unpack(r.x); f[1] = H::unpack(r.y); f[2] = H::unpack(r.z); f[3] = H::unpack(r.w);
@@ -98,7 +99,7 @@ template <typename T> struct Vec16x8 {
 template <typename T> struct Vec16x4 {
     using H = Half16<T>;
     uint2 r;
-    __device__ __forceinline__ void load(const T *p) { r = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void load(const T *p) { r = load_global(reinterpret_cast<const uint2 *>(p)); }
     __device__ __forceinline__ void zero() { r = make_uint2(0, 0); }
     __device__ __forceinline__ void to_f2(float2 (&f)[2]) const { f[0] = H::unpack(r.x); f[1] = H::unpack(r.y); }
     static __device__ __forceinline__ void store(T *p, const float2 (&f)[2]) {
@@ -110,7 +111,7 @@ template <typename T> struct Vec16x4 {
 template <typename T> struct Vec16x2 {
     using H = Half16<T>;
     uint32_t r;
-    __device__ __forceinline__ void load(const T *p) { r = __ldg(reinterpret_cast<const unsigned int *>(p)); }
+    __device__ __forceinline__ void load(const T *p) { r = load_global(reinterpret_cast<const unsigned int *>(p)); }
     __device__ __forceinline__ void zero() { r = 0; }
     __device__ __forceinline__ void to_f2(float2 (&f)[1]) const { f[0] = H::unpack(r); }
     static __device__ __forceinline__ void store(T *p, const float2 (&f)[1]) {
@@ -124,7 +125,7 @@ template <typename T> struct Vec16x2 {
 template <typename T> struct Vec16x1 {
     using H = Half16<T>;
     unsigned short r;
-    __device__ __forceinline__ void load(const T *p) { r = __ldg(reinterpret_cast<const unsigned short *>(p)); }
+    __device__ __forceinline__ void load(const T *p) { r = load_global(reinterpret_cast<const unsigned short *>(p)); }
     __device__ __forceinline__ void zero() { r = 0; }
     __device__ __forceinline__ void to_f2(float2 (&f)[1]) const { f[0] = make_float2(H::one(r), 0.f); }
     static __device__ __forceinline__ void store(T *p, const float2 (&f)[1]) { *p = H::cvt(f[0].x); }
@@ -142,7 +143,7 @@ template <> struct Vec<f16, 1> : Vec16x1<f16> {};
 
 template <> struct Vec<float, 4> {
     float4 r;
-    __device__ __forceinline__ void load(const float *p) { r = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void load(const float *p) { r = load_global(reinterpret_cast<const float4 *>(p)); }
     __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void to_f2(float2 (&f)[2]) const {
         f[0] = make_float2(r.x, r.y); f[1] = make_float2(r.z, r.w);
@@ -157,7 +158,7 @@ template <> struct Vec<float, 4> {
 
 template <> struct Vec<float, 2> {
     float2 r;
-    __device__ __forceinline__ void load(const float *p) { r = __ldg(reinterpret_cast<const float2 *>(p)); }
+    __device__ __forceinline__ void load(const float *p) { r = load_global(reinterpret_cast<const float2 *>(p)); }
     __device__ __forceinline__ void zero() { r = make_float2(0.f, 0.f); }
     __device__ __forceinline__ void to_f2(float2 (&f)[1]) const { f[0] = r; }
     static __device__ __forceinline__ void store(float *p, const float2 (&f)[1]) {
@@ -170,7 +171,7 @@ template <> struct Vec<float, 2> {
 
 template <> struct Vec<float, 1> {
     float r;
-    __device__ __forceinline__ void load(const float *p) { r = __ldg(p); }
+    __device__ __forceinline__ void load(const float *p) { r = load_global(p); }
     __device__ __forceinline__ void zero() { r = 0.f; }
     __device__ __forceinline__ void to_f2(float2 (&f)[1]) const { f[0] = make_float2(r, 0.f); }
     static __device__ __forceinline__ void store(float *p, const float2 (&f)[1]) { *p = f[0].x; }
@@ -195,10 +196,10 @@ inline auto with_dtype(int dtype, Fn &&fn) -> decltype(fn(float{})) {
 template <int V>
 __device__ __forceinline__ void load_param(const float *p, float2 (&f)[Pairs<V>::n]) {
     if constexpr (V == 1) {
-        f[0] = make_float2(__ldg(p), 0.f);
+        f[0] = make_float2(load_global(p), 0.f);
     } else {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) f[i] = __ldg(reinterpret_cast<const float2 *>(p) + i);
+        for (int i = 0; i < V / 2; ++i) f[i] = load_global(reinterpret_cast<const float2 *>(p) + i);
     }
 }
 

@@ -127,12 +127,9 @@ __device__ __forceinline__ void store_pairs(TO *p, const float2 (&v)[NPR], int n
 
 template <typename TO, bool VEC_STORE, int J, int RI, int NPR>
 __global__ void __launch_bounds__(kSubWarpsMax * 32, kSubMinBlocks)
-dw_subsample_kernel(const float *__restrict__ mel, const float *__restrict__ w0,
-                    const float *__restrict__ b0, const float *__restrict__ w1,
-                    const float *__restrict__ b1, TO *__restrict__ out,
-                    const int32_t *__restrict__ lengths, int32_t *__restrict__ out_lengths,
-                    int B, int Tn, int F, int C, int T2, int F2, int T4, int F4, int Pt, int nCG,
-                    int nJB, int nRC) {
+dw_subsample_kernel(const float *mel, const float *w0, const float *b0, const float *w1, const float *b1,
+                    TO *__restrict__ out, const int32_t *lengths, int32_t *__restrict__ out_lengths, int B, int Tn,
+                    int F, int C, int T2, int F2, int T4, int F4, int Pt, int nCG, int nJB, int nRC) {
     constexpr int NMR = 4 * RI + 3;   // mel rows a block reads
     constexpr int W = 4 * J + 8;      // staged mel columns: [4 j0 - 4, 4 j0 + 4 J + 4)
     constexpr int CW = 64 * NPR;      // channels per warp
@@ -174,7 +171,7 @@ dw_subsample_kernel(const float *__restrict__ mel, const float *__restrict__ w0,
             const int rr = e / W, cc = e % W;
             const int mr = mrow0 + rr, mc = mcol0 + cc;
             float v = 0.f;
-            if (mr >= 0 && mr < L && mc >= 0 && mc < F) v = __ldg(melb + mr * F + mc);  // frames >= len read as 0
+            if (mr >= 0 && mr < L && mc >= 0 && mc < F) v = load_global(melb + mr * F + mc);  // frames >= len read as 0
             stage_mel(sm[rr][cc], v);
         }
     }
@@ -195,7 +192,7 @@ dw_subsample_kernel(const float *__restrict__ mel, const float *__restrict__ w0,
 
     float2 w0r[9][NPR], w1r[9][NPR], b0r[NPR], b1r[NPR];
     {
-        auto ld = [&](const float *p, int k) { return k < nvalid ? __ldg(p + k) : 0.f; };
+        auto ld = [&](const float *p, int k) { return k < nvalid ? load_global(p + k) : 0.f; };
 #pragma unroll
         for (int q = 0; q < NPR; ++q) {
 #pragma unroll
@@ -387,8 +384,8 @@ cudaError_t subsample_launch(const SubsampleArgs &a, bool tensor_cores, cudaStre
 #undef DW_SUB_LAUNCH
 }
 
-__global__ void dw_out_lengths_kernel(const int32_t *__restrict__ lengths, int32_t *__restrict__ out_lengths,
-                                      int64_t B, int64_t Tn) {
+__global__ void dw_out_lengths_kernel(const int32_t *lengths, int32_t *__restrict__ out_lengths, int64_t B,
+                                      int64_t Tn) {
     const int64_t b = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (b >= B) return;
     const int64_t L = clamp_len(lengths, b, Tn);

@@ -53,14 +53,14 @@ template <typename TD, bool VEC>
 __device__ __forceinline__ float2 load_dout(const TD *p, bool two) {
     if constexpr (VEC) {
         if constexpr (sizeof(TD) == 2) {
-            return Half16<TD>::unpack(__ldg(reinterpret_cast<const unsigned int *>(p)));
+            return Half16<TD>::unpack(load_global(reinterpret_cast<const unsigned int *>(p)));
         } else {
-            return __ldg(reinterpret_cast<const float2 *>(p));
+            return load_global(reinterpret_cast<const float2 *>(p));
         }
     } else {
         auto f = [](const TD *q) -> float {
             if constexpr (sizeof(TD) == 2) return static_cast<float>(*q);
-            else return __ldg(q);
+            else return load_global(q);
         };
         return make_float2(f(p), two ? f(p + 1) : 0.f);
     }
@@ -150,10 +150,9 @@ __device__ __forceinline__ void row_pass(int r, int R0, int S0, int send, int Pt
 #endif
 template <typename TD, bool VEC>
 __global__ void __launch_bounds__(kSbThreads, DW_SB_MINB)
-dw_subsample_bwd_kernel(const float *__restrict__ mel, const float *__restrict__ w0, const float *__restrict__ b0,
-                        const float *__restrict__ w1, const TD *__restrict__ dout,
-                        const int32_t *__restrict__ lengths, float *__restrict__ partials, int B, int Tn, int F,
-                        int C, int T2, int F2, int T4, int F4, int Pt, int nRT, int nST, int nCG) {
+dw_subsample_bwd_kernel(const float *mel, const float *w0, const float *b0, const float *w1, const TD *dout,
+                        const int32_t *lengths, float *__restrict__ partials, int B, int Tn, int F, int C, int T2,
+                        int F2, int T4, int F4, int Pt, int nRT, int nST, int nCG) {
     using W = typename DWord<TD>::type;
     __shared__ __align__(16) float2 sm[kSbMR][kSbMC];
     extern __shared__ __align__(16) unsigned char dyn_smem[];
@@ -161,7 +160,7 @@ dw_subsample_bwd_kernel(const float *__restrict__ mel, const float *__restrict__
     const int cg = blockIdx.x % nCG, g = blockIdx.x / nCG, G = gridDim.x / nCG;
     const int c = (cg * kSbThreads + threadIdx.x) * 2;  // this thread's first channel
     const bool act = c < C, two = c + 1 < C;
-    auto ld = [&](const float *p) { return make_float2(act ? __ldg(p) : 0.f, two ? __ldg(p + 1) : 0.f); };
+    auto ld = [&](const float *p) { return make_float2(act ? load_global(p) : 0.f, two ? load_global(p + 1) : 0.f); };
 
     float2 W0[9], W1[9], bias0;
 #pragma unroll
@@ -189,7 +188,7 @@ dw_subsample_bwd_kernel(const float *__restrict__ mel, const float *__restrict__
         for (int e = threadIdx.x; e < kSbMR * kSbMC; e += kSbThreads) {
             const int rr = e / kSbMC, cc = e % kSbMC;
             const int t = 2 * R0 - Pt + rr, f = 2 * S0 - 1 + cc;
-            const float v = (t >= 0 && t < L && f >= 0 && f < F) ? __ldg(mb + static_cast<int64_t>(t) * F + f) : 0.f;
+            const float v = (t >= 0 && t < L && f >= 0 && f < F) ? load_global(mb + static_cast<int64_t>(t) * F + f) : 0.f;
             sm[rr][cc] = make_float2(v, v);
         }
         __syncthreads();
@@ -236,15 +235,15 @@ dw_subsample_bwd_kernel(const float *__restrict__ mel, const float *__restrict__
 
 // Sum of the partial rows in a fixed order: 8 row groups per column, then a fixed tree.
 __global__ void __launch_bounds__(256)
-dw_subsample_bwd_finalize_kernel(const float *__restrict__ partials, int G, int C, float *__restrict__ dw0,
-                                 float *__restrict__ db0, float *__restrict__ dw1, float *__restrict__ db1) {
+dw_subsample_bwd_finalize_kernel(const float *partials, int G, int C, float *__restrict__ dw0, float *__restrict__ db0,
+                                 float *__restrict__ dw1, float *__restrict__ db1) {
     __shared__ float red[8][33];
     const int col = threadIdx.x % 32, rg = threadIdx.x / 32;
     const int64_t E = static_cast<int64_t>(kSbSlots) * C;
     const int64_t e = static_cast<int64_t>(blockIdx.x) * 32 + col;
     float s = 0.f;
     if (e < E) {
-        for (int r = rg; r < G; r += 8) s += __ldg(partials + static_cast<int64_t>(r) * E + e);
+        for (int r = rg; r < G; r += 8) s += load_global(partials + static_cast<int64_t>(r) * E + e);
     }
     red[rg][col] = s;
     __syncthreads();
@@ -265,8 +264,8 @@ dw_subsample_bwd_finalize_kernel(const float *__restrict__ partials, int G, int 
 // added in a fixed tree.  Launched programmatically after the partial kernel.
 constexpr int kSbFinGroups = 16, kSbMaxRows4 = 256;
 __global__ void __launch_bounds__(256)
-dw_subsample_bwd_finalize4_kernel(const float *__restrict__ partials, int G, int C, float *__restrict__ dw0,
-                                  float *__restrict__ db0, float *__restrict__ dw1, float *__restrict__ db1) {
+dw_subsample_bwd_finalize4_kernel(const float *partials, int G, int C, float *__restrict__ dw0, float *__restrict__ db0,
+                                  float *__restrict__ dw1, float *__restrict__ db1) {
     __shared__ float4 red[kSbFinGroups][16];
     launch_dependents();     // the next kernel may start its own set-up
     grid_dependency_wait();  // the partial rows are complete and visible after this
@@ -280,7 +279,7 @@ dw_subsample_bwd_finalize4_kernel(const float *__restrict__ partials, int G, int
 #pragma unroll
         for (int i = 0; i < kSbMaxRows4 / kSbFinGroups; ++i) {
             const int r = rg + i * kSbFinGroups;
-            v[i] = r < G ? __ldg(p4 + static_cast<int64_t>(r) * E4 + e4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = r < G ? load_global(p4 + static_cast<int64_t>(r) * E4 + e4) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int i = 0; i < kSbMaxRows4 / kSbFinGroups; ++i) {

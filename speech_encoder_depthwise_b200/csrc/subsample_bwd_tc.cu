@@ -179,10 +179,9 @@ __device__ __forceinline__ float2 pos_sel(float2 z, float2 v) {
 
 template <typename TD, bool PT1>
 __global__ void __launch_bounds__(kThreads, 1)
-dw_subsample_bwd_tc_kernel(const float *__restrict__ mel, const float *__restrict__ w0, const float *__restrict__ b0,
-                           const float *__restrict__ w1, const int32_t *__restrict__ lengths,
-                           const __grid_constant__ CUtensorMap dout_map, float *__restrict__ partials, int B,
-                           int Tn, int F, int C, int F2, int nRB, int nCB, int nG) {
+dw_subsample_bwd_tc_kernel(const float *mel, const float *w0, const float *b0, const float *w1, const int32_t *lengths,
+                           const __grid_constant__ CUtensorMap dout_map, float *__restrict__ partials, int B, int Tn,
+                           int F, int C, int F2, int nRB, int nCB, int nG) {
     constexpr int Pt = PT1 ? 1 : 2;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -257,11 +256,11 @@ dw_subsample_bwd_tc_kernel(const float *__restrict__ mel, const float *__restric
             float hi[9], lo[9];
 #pragma unroll
             for (int t = 0; t < 9; ++t) {
-                const float x = c < C ? __ldg(w0 + t * C + c) : 0.f;
+                const float x = c < C ? load_global(w0 + t * C + c) : 0.f;
                 hi[t] = tf32_hi(x);
                 lo[t] = x - hi[t];
             }
-            const float bx = c < C ? __ldg(b0 + c) : 0.f;
+            const float bx = c < C ? load_global(b0 + c) : 0.f;
             const float bhi = tf32_hi(bx);
             float4 q[8];
             q[0] = make_float4(hi[0], hi[1], hi[2], hi[3]);
@@ -299,7 +298,7 @@ dw_subsample_bwd_tc_kernel(const float *__restrict__ mel, const float *__restric
         float2 W[3][3], gw1[3][3];
 #pragma unroll
         for (int t = 0; t < 9; ++t) {
-            const float x = c < C ? __ldg(w1 + t * C + c) : 0.f;
+            const float x = c < C ? load_global(w1 + t * C + c) : 0.f;
             W[t / 3][t % 3] = make_float2(x, x);
             gw1[t / 3][t % 3] = make_float2(0.f, 0.f);
         }
@@ -486,7 +485,7 @@ dw_subsample_bwd_tc_kernel(const float *__restrict__ mel, const float *__restric
             for (int k = 0; k < kWinLoads; ++k) {
                 const int mr = mr0 + (wrc[k] >> 8), mc = mc0 + (wrc[k] & 255);
                 const bool in = wrc[k] >= 0 && mr >= 0 && mr < L && mc >= 0 && mc < F;
-                mv[k] = in ? __ldg(base + static_cast<int64_t>(mr) * F + mc) : 0.f;
+                mv[k] = in ? load_global(base + static_cast<int64_t>(mr) * F + mc) : 0.f;
             }
         };
         if (nA > 0) load_win(ulist[0]);

@@ -198,9 +198,8 @@ __device__ __forceinline__ float2 relu_pair(float a, float b) { return make_floa
 
 template <typename TO, int CTG>
 __global__ void __launch_bounds__(kThreads, 1)
-dw_subsample_tc_kernel(const float *__restrict__ mel, const float *__restrict__ w0, const float *__restrict__ b0,
-                       const float *__restrict__ w1, const float *__restrict__ b1,
-                       const int32_t *__restrict__ lengths, int32_t *__restrict__ out_lengths,
+dw_subsample_tc_kernel(const float *mel, const float *w0, const float *b0, const float *w1, const float *b1,
+                       const int32_t *lengths, int32_t *__restrict__ out_lengths,
                        const __grid_constant__ CUtensorMap out_map, int B, int Tn, int F, int C, int F2, int Pt,
                        int nIP, int nJB, int nG) {
     using Lay = TcLayout<TO, CTG>;
@@ -408,7 +407,7 @@ dw_subsample_tc_kernel(const float *__restrict__ mel, const float *__restrict__ 
         for (int i = 0; i < CTG; ++i) {
             const int c = (g * CTG + i) * 128 + r;
 #pragma unroll
-            for (int t = 0; t < 10; ++t) xw[i][t] = c < C ? __ldg(t < 9 ? w0 + t * C + c : b0 + c) : 0.f;
+            for (int t = 0; t < 10; ++t) xw[i][t] = c < C ? load_global(t < 9 ? w0 + t * C + c : b0 + c) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < CTG; ++i) {
@@ -449,7 +448,7 @@ dw_subsample_tc_kernel(const float *__restrict__ mel, const float *__restrict__ 
         for (int j = 0; j < kWtPer; ++j) {
             const int e = threadIdx.x + j * kEpiThreads;
             const int ct = e / 1280, t = (e / 128) % 10, c = (g * CTG + ct) * 128 + e % 128;
-            wv[j] = c < C ? __ldg(t < 9 ? w1 + t * C + c : b1 + c) : 0.f;
+            wv[j] = c < C ? load_global(t < 9 ? w1 + t * C + c : b1 + c) : 0.f;
         }
         TO *z = stage + 4 * kStElems;  // the zero tile stored for fully masked units
         for (int e = threadIdx.x; e < kStElems; e += kEpiThreads) stage_out<TO>(z + e, 0.f);

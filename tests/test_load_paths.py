@@ -19,23 +19,8 @@ def code(name):
         return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
 
 
-def function(text, name):
-    """The body of the first function of that name."""
-    at = text.index("{", text.index(name + "("))
-    depth = 0
-    for i in range(at, len(text)):
-        depth += {"{": 1, "}": -1}.get(text[i], 0)
-        if depth == 0:
-            return text[at:i + 1]
-
-
-@pytest.mark.parametrize("name", ["dropout.cu", "dropout.cuh", "residual.cuh", "layernorm_fwd.cu", "layernorm_fwd.cuh",
-                                  "layernorm_bwd.cu", "layernorm_bwd.cuh"])
-def test_residual_path_reads_nothing_as_read_only(name):
-    """Activations, parameters, lengths, generator state and partial rows."""
+@pytest.mark.parametrize("name", sorted(n for n in os.listdir(build.CSRC) if n.endswith((".cu", ".cuh"))))
+def test_kernels_read_nothing_as_read_only(name):
+    """Activations, parameters, lengths, generator state and partial rows: an earlier call may have written any of
+    them (out_lengths, weight gradients, a finalize kernel's partial rows)."""
     assert re.findall(READ_ONLY, code(name)) == []
-
-
-def test_lengths_are_not_read_as_read_only():
-    """An earlier call may write them: dw_subsample_fwd and dwconv2d_fwd do (out_lengths)."""
-    assert re.findall(READ_ONLY, function(code("dw_common.cuh"), "clamp_len")) == []

@@ -114,3 +114,73 @@ def test_parameters_and_lengths_that_the_call_before_wrote(T, C, dtype):
             dw.dw_dropout_add_fwd(y[i], x, h, rng, 0.5, 1.0, ln)
             after()
     check_graph(run, [y, z], [(ga, gamma), (be, beta), (ln, torch.full_like(ln, T)), (h, x), (dx, x)])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,C,K,offset", [(1, 512, 9, 0), (16, 512, 31, 0), (40, 519, 9, 0), (300, 64, 9, 0), (33, 130, 40, 1)])
+def test_convs_read_what_the_norm_before_wrote(T, C, K, offset, dtype):
+    """norm -> streaming conv -> conv -> its gradients, thirty steps through the same buffers, workspace and cache."""
+    B, steps = 8, 30
+    torch.manual_seed(C + K)
+    shape = (B, T, C)
+    src = torch.randn(steps, *shape, device="cuda").to(dtype)
+    w, bias = torch.randn(K, C, device="cuda") / K, torch.randn(C, device="cuda")
+    x, u, v, dx = (off_boundary(shape, dtype, offset) for _ in range(4))
+    cache = off_boundary((B, K - 1, C), dtype, offset)
+    m, r = torch.empty(B, T, device="cuda"), torch.empty(B, T, device="cuda")
+    ln = torch.tensor([T, T // 2, T, 0, 1, T, T, T], dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(16, dw.dwconv1d_bwd_dw_workspace_size(B, T, C, K)), dtype=torch.uint8, device="cuda")
+    gw, gb = torch.empty(steps, K, C, device="cuda"), torch.empty(steps, C, device="cuda")
+    y = torch.empty(steps, *shape, dtype=dtype, device="cuda")
+
+    def run(after):
+        for i in range(steps):
+            dw.dw_layernorm_fwd(src[i], None, None, x, m, r, ln, EPS)
+            after()
+            dw.dwconv1d_stream_fwd(x, w, bias, u, cache, ln)
+            after()
+            dw.dwconv1d_fwd(u, w, bias, v, ln, K // 2)
+            after()
+            dw.dwconv1d_bwd_dx(v, w, dx, ln, K // 2)
+            after()
+            dw.dwconv1d_bwd_dw(v, dx, gw[i], gb[i], ln, K // 2, ws)
+            after()
+            dw.dw_layernorm_fwd(dx, None, gb[i], y[i], None, None, ln, EPS)
+            after()
+    check_graph(run, [gw, gb, y], [(cache, torch.zeros_like(cache))])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("C,k,stride,offset", [(64, 3, 2, 0), (63, 3, 2, 0), (64, 5, 1, 0), (64, 3, 1, 1)])
+def test_conv2d_and_subsampler_read_what_the_norm_before_wrote(C, k, stride, offset, dtype):
+    """norm -> conv2d -> its gradients, and norm -> subsampler backward, twenty steps through the same buffers."""
+    B, T, F, steps = 2, 40, 10, 20
+    torch.manual_seed(C + k)
+    st, pads = (stride, stride), (k // 2,) * 3
+    To, Fo = dw.conv2d_out_shape(T, F, k, k, st, pads)
+    src = torch.randn(steps, B, T, F * C, device="cuda").to(dtype)
+    w, bias = torch.randn(k, k, C, device="cuda") / k, torch.randn(C, device="cuda")
+    x, dx = (off_boundary((B, T, F, C), dtype, offset) for _ in range(2))
+    v = off_boundary((B, To, Fo, C), dtype, offset)
+    ln, ol = torch.tensor([T, 17], dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(16, dw.dwconv2d_bwd_dw_workspace_size(B, T, F, C, k, k, st, pads)), dtype=torch.uint8, device="cuda")
+    gw, gb = torch.empty(steps, k, k, C, device="cuda"), torch.empty(steps, C, device="cuda")
+    mel, w0, b0, w1 = (torch.randn(s, device="cuda") for s in ((B, 4 * T, 4 * F), (3, 3, C), (C,), (3, 3, C)))
+    assert dw.subsample_out_shape(4 * T, 4 * F) == (T, F)
+    wsb = torch.empty(dw.dw_subsample_bwd_workspace_size(B, 4 * T, 4 * F, C), dtype=torch.uint8, device="cuda")
+    mln = torch.tensor([4 * T, 71], dtype=torch.int32, device="cuda")
+    g = [[torch.empty_like(t) for t in (w0, b0, w1, b0)] for _ in range(steps)]
+
+    def run(after):
+        for i in range(steps):
+            dw.dw_layernorm_fwd(src[i], None, None, x.view(B, T, F * C), None, None, ln, EPS)
+            after()
+            dw.dwconv2d_fwd(x, w, bias, v, ln, ol, st, pads)
+            after()
+            dw.dwconv2d_bwd_dx(v, w, dx, ln, st, pads)
+            after()
+            dw.dwconv2d_bwd_dw(dx, v, gw[i], gb[i], ln, st, pads, ws)
+            after()
+            dw.dw_subsample_bwd(mel, w0, b0, w1, x, mln, *g[i], False, wsb)
+            after()
+    check_graph(run, [gw, gb] + [t for s in g for t in s], [])
