@@ -28,8 +28,9 @@
  *  - Errors: every call returns a dw_status_t and never aborts or traps.  Argument errors
  *    are found on the host before any CUDA call.  A failed launch returns DW_ERR_CUDA.
  *    C above 4,194,304 channels or K above 4096 returns DW_ERR_UNSUPPORTED.
- *    B == 0 or T == 0 is a valid no-op.  Misaligned pointers, or a C that is not a
- *    multiple of the vector width, take a narrower (slower) path and stay correct.
+ *    B == 0 or T == 0 is a valid no-op.  Pointers off a vector's boundary, or a C that is
+ *    not a multiple of the vector width, take a narrower (slower) path and stay correct; a
+ *    pointer that is not a multiple of its element's size returns DW_ERR_INVALID_ARG.
  *  - Arithmetic: bf16, fp16 or float32 I/O, float32 accumulation, 16-bit stores rounded to
  *    nearest even.  The subsampler's conv0 runs on the tensor cores (float32-accurate split),
  *    and so do its backward's conv0 recompute and dw0/db0 reduction; everything else runs on the
@@ -425,11 +426,11 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
  *  - A packed batch [N][C] is B = 1, T = N with `lengths` pointing at its last offset
  *    (offsets + B): rows no sequence covers are then written as zeros.  A streaming step of B
  *    streams with one frame each is T = 1.
- *  - Any C from 1 to 4,194,304 and any alignment.  Up to 8199 channels take the vector kernels when
- *    all activations of a call lie the same number of elements past a boundary of 8 elements (none
- *    where a mask is drawn), whether or not the rows after the first start on 16 bytes; so do
- *    longer rows of a multiple of 8 channels, up to 51200 (backward 25600), on such a boundary.
- *    Other calls take a narrower (slower) kernel.
+ *  - Any C from 1 to 4,194,304 and any alignment to whole elements.  Up to 8199 channels take the
+ *    vector kernels when all activations of a call lie the same number of elements past a boundary
+ *    of 8 elements (none where a mask is drawn), whether or not the rows after the first start on
+ *    16 bytes; so do longer rows of a multiple of 8 channels, up to 51200 (backward 25600), on such
+ *    a boundary.  Other calls take a narrower (slower) kernel.
  *  - Dropout: rng points at two device uint64, {seed, offset}, read when the kernel runs, so a
  *    captured graph draws new numbers once the program changes them on the device.  Element e
  *    of the tensor (its flat index, from 0) uses the 16 bits number e mod 8 (word (e mod 8)/2,

@@ -32,6 +32,7 @@ using dwapi::aligned;
 using dwapi::dtype_size;
 using dwapi::kMaxChannels;
 using dwapi::mul3;
+using dwapi::on_elements;
 using dwapi::overlaps;
 using dwapi::valid_dtype;
 
@@ -50,14 +51,16 @@ int pick_vec_width(int64_t C, size_t esize, std::initializer_list<const void *> 
     return 1;
 }
 
-dw_status_t check_conv1d_common(const void *in, const float *w, const void *out, int64_t B, int64_t T,
-                                int64_t C, int K, int pad_left, dw_dtype_t dt, int64_t *n) {
+dw_status_t check_conv1d_common(const void *in, const float *w, const float *bias, const void *out,
+                                const int32_t *lengths, int64_t B, int64_t T, int64_t C, int K, int pad_left,
+                                dw_dtype_t dt, int64_t *n) {
     if (!valid_dtype(dt)) return DW_ERR_INVALID_ARG;
     if (B < 0 || T < 0 || C < 1 || K < 1 || pad_left < 0 || pad_left > K - 1) return DW_ERR_INVALID_ARG;
     if (C > kMaxChannels || K > 4096) return DW_ERR_UNSUPPORTED;
     if (!mul3(B, T, C, n)) return DW_ERR_INVALID_ARG;
     if (*n == 0) return DW_OK;
     if (in == nullptr || w == nullptr || out == nullptr) return DW_ERR_INVALID_ARG;
+    if (!on_elements(dtype_size(dt), {in, out}) || !on_elements(4, {w, bias, lengths})) return DW_ERR_INVALID_ARG;
     const size_t bytes = static_cast<size_t>(*n) * dtype_size(dt);
     if (overlaps(in, bytes, out, bytes)) return DW_ERR_INVALID_ARG;
     return DW_OK;
@@ -97,10 +100,10 @@ dwk::Conv2dArgs conv2d_args(int64_t B, int64_t T, int64_t F, int64_t C, int64_t 
 }
 
 // Packed sequences: x/y [N][C], item b on rows offsets[b] .. offsets[b+1]-1.
-dw_status_t packed_common(const void *in, const float *w, void *out, const int32_t *offsets, int64_t B, int64_t N,
-                          int64_t C, int K, int pad_left, dw_dtype_t dt, dwk::Conv1dArgs *a) {
+dw_status_t packed_common(const void *in, const float *w, const float *bias, void *out, const int32_t *offsets,
+                          int64_t B, int64_t N, int64_t C, int K, int pad_left, dw_dtype_t dt, dwk::Conv1dArgs *a) {
     int64_t n = 0;
-    dw_status_t st = check_conv1d_common(in, w, out, 1, N, C, K, pad_left, dt, &n);
+    dw_status_t st = check_conv1d_common(in, w, bias, out, offsets, 1, N, C, K, pad_left, dt, &n);
     if (st != DW_OK) return st;
     if (B < 0) return DW_ERR_INVALID_ARG;
     if (N >= (int64_t(1) << 30) || B >= (int64_t(1) << 30)) return DW_ERR_UNSUPPORTED;  // 32-bit row indices
@@ -123,7 +126,11 @@ dw_status_t bwd_dw_prepare(const void *x, const void *dy, float *dw, float *dbia
     if (!mul3(B, T, C, n)) return DW_ERR_INVALID_ARG;
     if (dw == nullptr) return DW_ERR_INVALID_ARG;
     if (static_cast<int64_t>(K + 1) * C > dwk::kMaxGrid * 256LL) return DW_ERR_INVALID_ARG;
-    if (*n > 0 && (x == nullptr || dy == nullptr)) return DW_ERR_INVALID_ARG;
+    if (!on_elements(4, {dw, dbias})) return DW_ERR_INVALID_ARG;
+    if (*n > 0) {
+        if (x == nullptr || dy == nullptr) return DW_ERR_INVALID_ARG;
+        if (!on_elements(dtype_size(io_dtype), {x, dy}) || !on_elements(4, {lengths})) return DW_ERR_INVALID_ARG;
+    }
     a->x = x; a->dy = dy; a->dw = dw; a->dbias = dbias; a->lengths = lengths;
     a->B = B; a->T = T; a->C = C; a->K = K; a->pad_left = pad_left;
     a->dtype = static_cast<int>(io_dtype);
@@ -151,7 +158,7 @@ const char *dw_status_string(dw_status_t s) {
 int dw_last_cuda_error(void) { return g_last_cuda_error; }
 
 dw_status_t dw_selftest_wait_timeout(int *done, dw_stream_t stream) {
-    if (done == nullptr) return DW_ERR_INVALID_ARG;
+    if (done == nullptr || !on_elements(4, {done})) return DW_ERR_INVALID_ARG;
     return cuda_status(dwk::selftest_wait_timeout_launch(done, static_cast<cudaStream_t>(stream)));
 }
 
@@ -166,7 +173,7 @@ dw_status_t dwconv1d_fwd(const void *x, const float *w, const float *bias, void 
                          int64_t B, int64_t T, int64_t C, int K, int pad_left, dw_dtype_t io_dtype,
                          dw_stream_t stream) {
     int64_t n = 0;
-    dw_status_t st = check_conv1d_common(x, w, y, B, T, C, K, pad_left, io_dtype, &n);
+    dw_status_t st = check_conv1d_common(x, w, bias, y, lengths, B, T, C, K, pad_left, io_dtype, &n);
     if (st != DW_OK || n == 0) return st;
     dwk::Conv1dArgs a;
     a.x = x; a.w = w; a.bias = bias; a.y = y; a.lengths = lengths;
@@ -179,7 +186,7 @@ dw_status_t dwconv1d_fwd(const void *x, const float *w, const float *bias, void 
 dw_status_t dwconv1d_bwd_dx(const void *dy, const float *w, void *dx, const int32_t *lengths, int64_t B,
                             int64_t T, int64_t C, int K, int pad_left, dw_dtype_t io_dtype, dw_stream_t stream) {
     int64_t n = 0;
-    dw_status_t st = check_conv1d_common(dy, w, dx, B, T, C, K, pad_left, io_dtype, &n);
+    dw_status_t st = check_conv1d_common(dy, w, nullptr, dx, lengths, B, T, C, K, pad_left, io_dtype, &n);
     if (st != DW_OK || n == 0) return st;
     dwk::Conv1dArgs a;
     a.x = dy; a.w = w; a.bias = nullptr; a.y = dx; a.lengths = lengths;
@@ -195,10 +202,10 @@ dw_status_t dwconv1d_bwd(const void *x, const void *dy, const float *w, void *dx
                          const int32_t *lengths, int64_t B, int64_t T, int64_t C, int K, int pad_left,
                          dw_dtype_t io_dtype, void *workspace, size_t workspace_bytes, dw_stream_t stream) {
     int64_t n = 0;
-    dw_status_t st = check_conv1d_common(dy, w, dx, B, T, C, K, pad_left, io_dtype, &n);
+    dw_status_t st = check_conv1d_common(dy, w, nullptr, dx, lengths, B, T, C, K, pad_left, io_dtype, &n);
     if (st != DW_OK) return st;
     if (n > 0) {
-        if (x == nullptr) return DW_ERR_INVALID_ARG;
+        if (x == nullptr || !on_elements(dtype_size(io_dtype), {x})) return DW_ERR_INVALID_ARG;
         const size_t bytes = static_cast<size_t>(n) * dtype_size(io_dtype);
         if (overlaps(dx, bytes, x, bytes)) return DW_ERR_INVALID_ARG;
     }
@@ -206,7 +213,7 @@ dw_status_t dwconv1d_bwd(const void *x, const void *dy, const float *w, void *dx
     if (n == 0)
         return dwconv1d_bwd_dw(x, dy, dw, dbias, lengths, B, T, C, K, pad_left, io_dtype, workspace,
                                workspace_bytes, stream);
-    if (dw == nullptr) return DW_ERR_INVALID_ARG;
+    if (dw == nullptr || !on_elements(4, {dw, dbias})) return DW_ERR_INVALID_ARG;
     const size_t need = dwk::conv1d_dw_workspace_bytes(B, T, C, K);
     if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)) return DW_ERR_WORKSPACE;
     const size_t out_bytes = static_cast<size_t>(K) * C * sizeof(float);
@@ -235,7 +242,7 @@ dw_status_t dwconv1d_fwd_packed(const void *x, const float *w, const float *bias
                                 int64_t B, int64_t N, int64_t C, int K, int pad_left, dw_dtype_t io_dtype,
                                 dw_stream_t stream) {
     dwk::Conv1dArgs a;
-    dw_status_t st = packed_common(x, w, y, offsets, B, N, C, K, pad_left, io_dtype, &a);
+    dw_status_t st = packed_common(x, w, bias, y, offsets, B, N, C, K, pad_left, io_dtype, &a);
     if (st != DW_OK || B == 0 || N == 0) return st;
     a.x = x; a.w = w; a.bias = bias; a.y = y; a.pad_left = pad_left; a.flip = 0;
     a.vec_width = pick_vec_width(C, dtype_size(io_dtype), {x, y}, {w, bias});
@@ -246,7 +253,7 @@ dw_status_t dwconv1d_bwd_dx_packed(const void *dy, const float *w, void *dx, con
                                    int64_t N, int64_t C, int K, int pad_left, dw_dtype_t io_dtype,
                                    dw_stream_t stream) {
     dwk::Conv1dArgs a;
-    dw_status_t st = packed_common(dy, w, dx, offsets, B, N, C, K, pad_left, io_dtype, &a);
+    dw_status_t st = packed_common(dy, w, nullptr, dx, offsets, B, N, C, K, pad_left, io_dtype, &a);
     if (st != DW_OK || B == 0 || N == 0) return st;
     a.x = dy; a.w = w; a.bias = nullptr; a.y = dx;
     a.pad_left = K - 1 - pad_left;  // correlation with reversed taps: the pads swap
@@ -271,7 +278,7 @@ dw_status_t dwconv1d_bwd_dw_packed(const void *x, const void *dy, float *dw, flo
     if (N >= (int64_t(1) << 30) || B >= (int64_t(1) << 30)) return DW_ERR_UNSUPPORTED;
     int64_t n = 0;
     if (!mul3(1, N, C, &n)) return DW_ERR_INVALID_ARG;
-    if (dw == nullptr) return DW_ERR_INVALID_ARG;
+    if (dw == nullptr || !on_elements(4, {dw, dbias})) return DW_ERR_INVALID_ARG;
     const size_t out_bytes = static_cast<size_t>(K) * C * sizeof(float), gb = static_cast<size_t>(C) * sizeof(float);
     if (dbias != nullptr && overlaps(dw, out_bytes, dbias, gb)) return DW_ERR_INVALID_ARG;
     dwk::DwArgs a;
@@ -283,6 +290,7 @@ dw_status_t dwconv1d_bwd_dw_packed(const void *x, const void *dy, float *dw, flo
     a.vec_width = 1;
     if (B > 0 && N > 0) {
         if (x == nullptr || dy == nullptr || offsets == nullptr) return DW_ERR_INVALID_ARG;
+        if (!on_elements(dtype_size(io_dtype), {x, dy}) || !on_elements(4, {offsets})) return DW_ERR_INVALID_ARG;
         const size_t need = dwk::conv1d_dw_packed_workspace_bytes(N, C, K);
         if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)) return DW_ERR_WORKSPACE;
         if (overlaps(workspace, need, dw, out_bytes) || (dbias && overlaps(workspace, need, dbias, gb)))
@@ -298,12 +306,12 @@ dw_status_t dwconv1d_stream_fwd(const void *x, const float *w, const float *bias
                                 const int32_t *lengths, int64_t B, int64_t T, int64_t C, int K,
                                 dw_dtype_t io_dtype, dw_stream_t stream) {
     int64_t n = 0;
-    dw_status_t st = check_conv1d_common(x, w, y, B, T, C, K, K - 1, io_dtype, &n);
+    dw_status_t st = check_conv1d_common(x, w, bias, y, lengths, B, T, C, K, K - 1, io_dtype, &n);
     if (st != DW_OK || n == 0) return st;
     const size_t es = dtype_size(io_dtype);
     const size_t cache_bytes = static_cast<size_t>(B) * static_cast<size_t>(K - 1) * static_cast<size_t>(C) * es;
     if (K > 1) {
-        if (cache == nullptr) return DW_ERR_INVALID_ARG;
+        if (cache == nullptr || !on_elements(es, {cache})) return DW_ERR_INVALID_ARG;
         const size_t bytes = static_cast<size_t>(n) * es;
         if (overlaps(cache, cache_bytes, x, bytes) || overlaps(cache, cache_bytes, y, bytes)) return DW_ERR_INVALID_ARG;
     }
@@ -362,7 +370,7 @@ dw_status_t dw_subsample_bwd(const float *mel, const float *w0, const float *b0,
     if (C > kMaxChannels) return DW_ERR_UNSUPPORTED;
     int64_t n = 0;
     if (!mul3(B, T, F, &n)) return DW_ERR_INVALID_ARG;
-    if (!dw0 || !db0 || !dw1 || !db1) return DW_ERR_INVALID_ARG;
+    if (!dw0 || !db0 || !dw1 || !db1 || !on_elements(4, {dw0, db0, dw1, db1})) return DW_ERR_INVALID_ARG;
     auto s2 = [](int64_t v) -> int64_t { return v >= 1 ? (v - 1) / 2 + 1 : 0; };
     const int64_t T4 = s2(s2(T)), F4 = s2(s2(F));
     int64_t nout = 0;
@@ -374,6 +382,8 @@ dw_status_t dw_subsample_bwd(const float *mel, const float *w0, const float *b0,
     a.B = B; a.T = T; a.F = F; a.C = C; a.causal = causal; a.dout_dtype = static_cast<int>(dout_dtype);
     if (nout > 0) {
         if (!mel || !w0 || !b0 || !w1 || !dout) return DW_ERR_INVALID_ARG;
+        if (!on_elements(4, {mel, w0, b0, w1, lengths}) || !on_elements(dtype_size(dout_dtype), {dout}))
+            return DW_ERR_INVALID_ARG;
         const size_t need = dwk::subsample_bwd_workspace_bytes(B, T, F, C);
         if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)) return DW_ERR_WORKSPACE;
         const size_t g = static_cast<size_t>(9) * C * sizeof(float), gb = static_cast<size_t>(C) * sizeof(float);
@@ -394,9 +404,11 @@ dw_status_t dwconv2d_fwd(const void *x, const float *w, const float *bias, void 
     if (st != DW_OK) return st;
     const int64_t nin = B * T * F * C, nout = B * To * Fo * C;
     if (nout == 0 && out_lengths == nullptr) return DW_OK;
+    if (!on_elements(4, {lengths, out_lengths})) return DW_ERR_INVALID_ARG;
     if (nout > 0) {
         if (x == nullptr || w == nullptr || y == nullptr) return DW_ERR_INVALID_ARG;
         const size_t es = dtype_size(io_dtype);
+        if (!on_elements(es, {x, y}) || !on_elements(4, {w, bias})) return DW_ERR_INVALID_ARG;
         if (overlaps(x, static_cast<size_t>(nin) * es, y, static_cast<size_t>(nout) * es)) return DW_ERR_INVALID_ARG;
     }
     if (B == 0) return DW_OK;
@@ -416,9 +428,10 @@ dw_status_t dwconv2d_bwd_dx(const void *dy, const float *w, void *dx, const int3
     const int64_t nin = B * T * F * C, nout = B * To * Fo * C;
     if (nin == 0) return DW_OK;
     if (dx == nullptr || w == nullptr) return DW_ERR_INVALID_ARG;
+    const size_t es = dtype_size(io_dtype);
+    if (!on_elements(es, {dx}) || !on_elements(4, {w, lengths})) return DW_ERR_INVALID_ARG;
     if (nout > 0) {
-        if (dy == nullptr) return DW_ERR_INVALID_ARG;
-        const size_t es = dtype_size(io_dtype);
+        if (dy == nullptr || !on_elements(es, {dy})) return DW_ERR_INVALID_ARG;
         if (overlaps(dy, static_cast<size_t>(nout) * es, dx, static_cast<size_t>(nin) * es)) return DW_ERR_INVALID_ARG;
     }
     dwk::Conv2dArgs a = conv2d_args(B, T, F, C, To, Fo, KT, KF, stride_t, stride_f, pad_t, pad_b, pad_f, io_dtype);
@@ -442,7 +455,7 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
     int64_t To = 0, Fo = 0;
     dw_status_t st = conv2d_geometry(B, T, F, C, KT, KF, stride_t, stride_f, pad_t, pad_b, pad_f, &To, &Fo);
     if (st != DW_OK) return st;
-    if (dw == nullptr) return DW_ERR_INVALID_ARG;
+    if (dw == nullptr || !on_elements(4, {dw, dbias})) return DW_ERR_INVALID_ARG;
     const int64_t ntap = static_cast<int64_t>(KT) * KF;
     if ((ntap + 1) * C > dwk::kMaxGrid * 32LL) return DW_ERR_INVALID_ARG;
     const size_t out_bytes = static_cast<size_t>(ntap) * C * sizeof(float), gb = static_cast<size_t>(C) * sizeof(float);
@@ -452,6 +465,7 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
     float *partials = nullptr;
     if (B * To * Fo > 0) {
         if (x == nullptr || dy == nullptr) return DW_ERR_INVALID_ARG;
+        if (!on_elements(dtype_size(io_dtype), {x, dy}) || !on_elements(4, {lengths})) return DW_ERR_INVALID_ARG;
         const size_t need = dwk::conv2d_dw_workspace_bytes(B, To, C, KT, KF);
         if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)) return DW_ERR_WORKSPACE;
         if (overlaps(workspace, need, dw, out_bytes) || (dbias && overlaps(workspace, need, dbias, gb)))
@@ -477,8 +491,11 @@ dw_status_t subsample_fwd(const float *mel, const float *w0, const float *b0, co
     int64_t nout = 0;
     if (!mul3(B, T4 * F4, C, &nout)) return DW_ERR_INVALID_ARG;
     if (out_lengths == nullptr && nout == 0) return DW_OK;
+    if (!on_elements(4, {lengths, out_lengths})) return DW_ERR_INVALID_ARG;
     if (nout > 0) {
         if (!mel || !w0 || !b0 || !w1 || !b1 || !out) return DW_ERR_INVALID_ARG;
+        if (!on_elements(4, {mel, w0, b0, w1, b1}) || !on_elements(dtype_size(out_dtype), {out}))
+            return DW_ERR_INVALID_ARG;
         if (overlaps(mel, static_cast<size_t>(n) * 4, out, static_cast<size_t>(nout) * dtype_size(out_dtype)))
             return DW_ERR_INVALID_ARG;
     }

@@ -3,6 +3,8 @@
 // of the weight/bias gradient.
 #pragma once
 
+#include <initializer_list>
+
 #include "dw_internal.h"
 #include "dwconv.h"
 
@@ -29,6 +31,14 @@ inline bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
 }
 
 inline bool aligned(const void *p, size_t n) { return p == nullptr || reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether every pointer lies on a multiple of its elements' size (absent ones do): a load of one that does not
+// would fault.
+inline bool on_elements(size_t esize, std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (!aligned(p, esize)) return false;
+    return true;
+}
 
 // Channel counts beyond this are rejected: frame offsets are kept in 32 bits inside a run.
 constexpr int64_t kMaxChannels = 1 << 22;

@@ -12,6 +12,7 @@ using dwapi::aligned;
 using dwapi::cuda_status;
 using dwapi::dtype_size;
 using dwapi::mul3;
+using dwapi::on_elements;
 using dwapi::overlaps;
 
 // The memory of one call: no output may overlap an input or another output.
@@ -32,13 +33,11 @@ bool disjoint(std::initializer_list<Region> outs, std::initializer_list<Region> 
 
 // How many elements past a boundary of 8 every activation lies, the same for all; -1 where they differ.
 int oct_phase(dw_dtype_t dt, std::initializer_list<const void *> acts) {
-    const uintptr_t es = dtype_size(dt);
     int phase = -1;
     for (const void *p : acts) {
         if (p == nullptr) continue;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-        const int k = at % es == 0 ? static_cast<int>(at / es % 8) : -1;
-        if (k < 0 || (phase >= 0 && k != phase)) return -1;
+        const int k = static_cast<int>(reinterpret_cast<uintptr_t>(p) / dtype_size(dt) % 8);
+        if (phase >= 0 && k != phase) return -1;
         phase = k;
     }
     return phase;
@@ -71,6 +70,9 @@ dw_status_t norm_fwd(dwk::ResidualArgs *a, int64_t n, float eps, dw_dtype_t dt, 
     if (!(eps >= 0.f) || !isfinite(eps)) return DW_ERR_INVALID_ARG;
     if (n == 0) return DW_OK;
     if (a->x == nullptr || a->y == nullptr) return DW_ERR_INVALID_ARG;
+    if (!on_elements(dtype_size(dt), {a->x, a->res, a->y, a->h}) ||
+        !on_elements(4, {a->gamma, a->beta, a->mean, a->rstd, a->lengths}))
+        return DW_ERR_INVALID_ARG;
     const size_t act = static_cast<size_t>(n) * dtype_size(dt), row = static_cast<size_t>(a->B * a->T) * sizeof(float),
                  par = static_cast<size_t>(a->C) * sizeof(float);
     if (!disjoint({{a->y, act}, {a->h, act}, {a->mean, row}, {a->rstd, row}},
@@ -88,8 +90,12 @@ dw_status_t norm_bwd(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, void *works
     const size_t act = static_cast<size_t>(n) * dtype_size(dt), row = static_cast<size_t>(a->B * a->T) * sizeof(float),
                  par = static_cast<size_t>(a->C) * sizeof(float);
     size_t need = 0;
+    if (!on_elements(4, {a->dgamma, a->dbeta})) return DW_ERR_INVALID_ARG;
     if (n > 0) {
         if (a->x == nullptr || a->dy == nullptr || a->mean == nullptr || a->rstd == nullptr || a->dx == nullptr)
+            return DW_ERR_INVALID_ARG;
+        if (!on_elements(dtype_size(dt), {a->x, a->dy, a->dh, a->dx, a->dres}) ||
+            !on_elements(4, {a->gamma, a->mean, a->rstd, a->lengths}))
             return DW_ERR_INVALID_ARG;
         if (params) {
             need = dwk::layernorm_bwd_workspace_bytes(a->B, a->T, a->C);
@@ -113,6 +119,7 @@ dw_status_t norm_bwd(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, void *works
 dw_status_t dropout_add(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, dw_stream_t stream) {
     if (n == 0) return DW_OK;
     if (a->x == nullptr || a->y == nullptr) return DW_ERR_INVALID_ARG;
+    if (!on_elements(dtype_size(dt), {a->x, a->res, a->y}) || !on_elements(4, {a->lengths})) return DW_ERR_INVALID_ARG;
     const size_t act = static_cast<size_t>(n) * dtype_size(dt);
     if (!disjoint({{a->y, act}}, {{a->x, act}, {a->res, act}, {a->rng, a->thr ? 16u : 0u},
                                   {a->lengths, static_cast<size_t>(a->B) * sizeof(int32_t)}}))
