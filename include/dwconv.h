@@ -31,6 +31,10 @@
  *    B == 0 or T == 0 is a valid no-op.  Pointers off a vector's boundary, or a C that is
  *    not a multiple of the vector width, take a narrower (slower) path and stay correct; a
  *    pointer that is not a multiple of its element's size returns DW_ERR_INVALID_ARG.
+ *  - Reproducibility: no sum uses atomics.  Where a result is called reproducible for given sizes on
+ *    a given GPU model, calls agree bit for bit when they agree in sizes, types and values, in which
+ *    operands are NULL, and in every pointer modulo 32 bytes.  Another alignment, or a NULL in
+ *    place of an operand, may select another kernel, whose sums run in another order.
  *  - Arithmetic: bf16, fp16 or float32 I/O, float32 accumulation, 16-bit stores rounded to
  *    nearest even.  The subsampler's conv0 runs on the tensor cores (float32-accurate split),
  *    and so do its backward's conv0 recompute and dw0/db0 reduction; everything else runs on the
@@ -474,7 +478,8 @@ size_t dw_layernorm_bwd_workspace_size(int64_t B, int64_t T, int64_t C);
  *   dgamma[c] = sum_{valid b,t} dy xh,   dbeta[c] = sum_{valid b,t} dy
  *
  * dgamma and dbeta: float32 partial sums per block go to `workspace` and a second kernel adds
- * them in a fixed order: bitwise reproducible for given sizes on a given GPU model.  No atomics.
+ * them in a fixed order: dx, dgamma and dbeta are bitwise reproducible for given sizes on a given GPU
+ * model (see Reproducibility above: pointer alignments and NULL operands belong to it).  No atomics.
  *
  *  x, dy          the forward pass's input and the gradient of y;  dx the gradient of x
  *  mean, rstd     [B][T] float32 from the forward pass

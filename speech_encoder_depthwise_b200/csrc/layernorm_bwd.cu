@@ -5,7 +5,8 @@
 //  1. row kernel: every block walks rows and adds their dgamma/dbeta terms to a partial row of its
 //     own in the workspace, [G][2][ceil4(C)];
 //  2. finalize kernel: the partial rows added in a fixed order.
-// No atomics: bitwise reproducible for given sizes on a given GPU model.
+// No atomics: bitwise reproducible for given sizes, pointer alignments and NULL operands on a given GPU model
+// (alignment and gamma choose the kernel, which orders a row's and the rows' sums).
 #include "dw_internal.h"
 #include "residual.cuh"
 

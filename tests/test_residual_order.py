@@ -184,3 +184,31 @@ def test_conv2d_and_subsampler_read_what_the_norm_before_wrote(C, k, stride, off
             dw.dw_subsample_bwd(mel, w0, b0, w1, x, mln, *g[i], False, wsb)
             after()
     check_graph(run, [gw, gb] + [t for s in g for t in s], [])
+
+
+@pytest.mark.parametrize("C", [512, 136, 519, 8200])
+@pytest.mark.parametrize("act,par", [(0, 0), (0, 1), (3, 0), (None, 0)])
+def test_reproducible_at_equal_alignment(C, act, par):
+    """The same values at other addresses with the same remainder modulo 32 bytes: every result bit for bit.
+    (act: elements past a boundary, None for inputs and outputs that differ; par: gamma's.)"""
+    B, T, dtype = 3, 700, torch.bfloat16
+    torch.manual_seed(C)
+    vx, vdy = (torch.randn(B, T, C, device="cuda").to(dtype) for _ in range(2))
+    vga, ln = torch.rand(C, device="cuda") + 0.5, torch.tensor([700, 211, 0], dtype=torch.int32, device="cuda")
+    m, r = vx.float().mean(-1), torch.rsqrt(vx.float().var(-1, unbiased=False) + EPS)
+    got, kept = [], []
+    for shift in (0, 16, 32):  # multiples of 32 bytes for both types
+        i, o = (act, act) if act is not None else (0, 1)
+        x, dy = (off_boundary((B, T, C), dtype, i + 2 * shift) for _ in range(2))
+        dx, ga = off_boundary((B, T, C), dtype, o + 2 * shift), off_boundary((C,), torch.float32, par + shift)
+        dg, db = (off_boundary((C,), torch.float32, shift) for _ in range(2))
+        ws = torch.empty(dw.dw_layernorm_bwd_workspace_size(B, T, C), dtype=torch.uint8, device="cuda")
+        for t, v in ((x, vx), (dy, vdy), (ga, vga)):
+            t.copy_(v)
+        dw.dw_layernorm_bwd(x, dy, ga, m, r, dx, dg, db, ln, ws)
+        got.append((dx, dg, db))
+        kept.append((x, dy, ga, ws))  # nothing is freed, so that no address comes back
+    torch.cuda.synchronize()
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
