@@ -430,8 +430,9 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, int *G, cudaStream_t
     if constexpr (!SHIFT) {
         if (n <= 8) return launch<T, 8, 1, SHIFT>(a, G, s);
         if (n <= 16) return launch<T, 8, 2, SHIFT>(a, G, s);
+    } else if (n <= 16) {
+        return launch<T, 16, 1, SHIFT>(a, G, s);
     }
-    if (n <= 16) return launch<T, 16, 1, SHIFT>(a, G, s);
     if (n <= 32) return launch<T, 16, 2, SHIFT>(a, G, s);
     if (n <= 64) return launch<T, 32, 2, SHIFT>(a, G, s);
     if (n <= 96) return launch<T, 32, 3, SHIFT>(a, G, s);

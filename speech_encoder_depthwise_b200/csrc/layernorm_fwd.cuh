@@ -252,9 +252,10 @@ cudaError_t launch_octets(const ResidualArgs &a, int64_t n, cudaStream_t s) {
             if (n <= 16) return launch<T, 8, 2, SHIFT>(a, s);
             if (n <= 24) return launch<T, 8, 3, SHIFT>(a, s);
             if (n <= 32) return launch<T, 8, 4, SHIFT>(a, s);
+        } else {
+            if (n <= 16) return launch<T, 16, 1, SHIFT>(a, s);
+            if (n <= 32) return launch<T, 16, 2, SHIFT>(a, s);
         }
-        if (n <= 16) return launch<T, 16, 1, SHIFT>(a, s);
-        if (n <= 32) return launch<T, 16, 2, SHIFT>(a, s);
         if (n <= 48) return launch<T, 16, 3, SHIFT>(a, s);
         if (n <= 64) return launch<T, 16, 4, SHIFT>(a, s);
         if (n <= 80) return launch<T, 16, 5, SHIFT>(a, s);
