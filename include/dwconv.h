@@ -444,7 +444,8 @@ dw_status_t dwconv2d_bwd_dw(const void *x, const void *dy, float *dw, float *dbi
  *    A dropped element counts as zero whatever it holds; a kept one is multiplied by
  *    m = alpha 65536 / (65536 - thr) (0 when thr = 65536), so the expectation is alpha x whatever
  *    the rounding of p.  No mask is stored: the backward pass draws it again from the same rng
- *    values, p and sizes.  alpha is the residual branch's factor (1, or 1/2 for a half-step
+ *    values, p and sizes.  The mask depends on nothing else, so two dropouts of one step need
+ *    different offsets (or seeds).  alpha is the residual branch's factor (1, or 1/2 for a half-step
  *    module).  0 <= p <= 1; with thr = 0 nothing is drawn and rng may be NULL.
  */
 
@@ -532,7 +533,9 @@ dw_status_t dw_dropout_add_layernorm_fwd(const void *x, const void *residual, co
  *
  *   ds = [t < len_b] (dh + dl),   dresidual = ds,   dx = [kept] m ds
  *
- * each rounded once from the float32 ds.
+ * each rounded once from the float32 ds.  xh is rebuilt from the stored h: its rounding moves xh by up
+ * to half a step of h times rstd (|h| rstd 2^-8 in bf16, 2^-11 in fp16, nothing in float32), which
+ * is small for rows around zero and grows with a row's mean over its deviation.
  *
  *  dy, dh      the gradients of y and of h (dh NULL: zeros)
  *  dresidual   may be NULL (not wanted)

@@ -505,7 +505,8 @@ def dw_layernorm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, lengths, works
 
 def dw_dropout_add_fwd(x, residual, y, rng, p, alpha, lengths, stream=None):
     """y = residual + alpha/(1-p) x on the kept elements of the valid frames, residual alone on the
-    dropped ones (residual may be None); ``rng`` is a CUDA int64 tensor {seed, offset}."""
+    dropped ones (residual may be None); ``rng`` is a CUDA int64 tensor {seed, offset}: the same one
+    gives the same mask, so each dropout of a step needs an offset of its own."""
     px, shape, dt, code, dev = _lead(x, "x")
     _, i32, i64 = _names[:3]
     _call("dw_dropout_add_fwd", dev, stream,
