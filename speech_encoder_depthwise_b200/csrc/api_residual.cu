@@ -60,6 +60,9 @@ dw_status_t set_dropout(const uint64_t *rng, double p, double alpha, int64_t n, 
     return DW_OK;
 }
 
+// The generator's state where the call reads it.
+const void *drawn(const dwk::ResidualArgs *a) { return a->thr > 0 ? a->rng : nullptr; }
+
 void set_sizes(dwk::ResidualArgs *a, const int32_t *lengths, int64_t B, int64_t T, int64_t C, dw_dtype_t dt) {
     a->lengths = lengths;
     a->B = B; a->T = T; a->C = C;
@@ -76,7 +79,7 @@ dw_status_t norm_fwd(dwk::ResidualArgs *a, int64_t n, float eps, dw_dtype_t dt, 
     const size_t act = static_cast<size_t>(n) * dtype_size(dt), row = static_cast<size_t>(a->B * a->T) * sizeof(float),
                  par = static_cast<size_t>(a->C) * sizeof(float);
     if (!disjoint({{a->y, act}, {a->h, act}, {a->mean, row}, {a->rstd, row}},
-                  {{a->x, act}, {a->res, act}, {a->gamma, par}, {a->beta, par}, {a->rng, a->thr ? 16u : 0u},
+                  {{a->x, act}, {a->res, act}, {a->gamma, par}, {a->beta, par}, {drawn(a), 16},
                    {a->lengths, static_cast<size_t>(a->B) * sizeof(int32_t)}}))
         return DW_ERR_INVALID_ARG;
     a->eps = eps;
@@ -110,7 +113,7 @@ dw_status_t norm_bwd(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, void *works
     const auto in = [&](const void *p) { return n > 0 ? p : nullptr; };
     if (!disjoint({{in(a->dx), act}, {in(a->dres), act}, {a->dgamma, par}, {a->dbeta, par}, {a->partials, need}},
                   {{in(a->x), act}, {in(a->dy), act}, {in(a->dh), act}, {in(a->gamma), par}, {in(a->mean), row},
-                   {in(a->rstd), row}, {in(a->rng), a->thr ? 16u : 0u},
+                   {in(a->rstd), row}, {in(drawn(a)), 16},
                    {in(a->lengths), static_cast<size_t>(a->B) * sizeof(int32_t)}}))
         return DW_ERR_INVALID_ARG;
     return cuda_status(dwk::layernorm_bwd_launch(*a, static_cast<cudaStream_t>(stream)));
@@ -121,7 +124,7 @@ dw_status_t dropout_add(dwk::ResidualArgs *a, int64_t n, dw_dtype_t dt, dw_strea
     if (a->x == nullptr || a->y == nullptr) return DW_ERR_INVALID_ARG;
     if (!on_elements(dtype_size(dt), {a->x, a->res, a->y}) || !on_elements(4, {a->lengths})) return DW_ERR_INVALID_ARG;
     const size_t act = static_cast<size_t>(n) * dtype_size(dt);
-    if (!disjoint({{a->y, act}}, {{a->x, act}, {a->res, act}, {a->rng, a->thr ? 16u : 0u},
+    if (!disjoint({{a->y, act}}, {{a->x, act}, {a->res, act}, {drawn(a), 16},
                                   {a->lengths, static_cast<size_t>(a->B) * sizeof(int32_t)}}))
         return DW_ERR_INVALID_ARG;
     a->phase = oct_phase(dt, {a->x, a->res, a->y});

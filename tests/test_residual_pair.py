@@ -63,3 +63,22 @@ def test_forward_and_backward_as_a_pair(B, T, C, dtype, mean, p):
     eg, eb = param_err(stored, c.dy, rm, rr, c.valid, per, G)
     assert_within("dgamma", dg.cpu().numpy(), rdg, 1.01 * eg + (np.abs(c.dy) * d * v).sum((0, 1)) + 1e-30)
     assert_within("dbeta", db.cpu().numpy(), rdb, eb + 1e-30)
+
+
+def test_generator_state_that_is_not_read_may_lie_anywhere():
+    """p = 0 draws nothing: rng may then be memory that the call writes."""
+    x = torch.randn(1, 4, 8, device="cuda")
+    y, h, dx = (torch.empty_like(x) for _ in range(3))
+    m, r = torch.empty(1, 4, device="cuda"), torch.empty(1, 4, device="cuda")
+
+    def inside(t):
+        return t.view(-1)[4:8].view(torch.int64)
+    dw.dw_dropout_add_fwd(x, None, y, inside(y), 0.0, 1.0, None)
+    assert torch.equal(y, x)
+    dw.dw_dropout_add_layernorm_fwd(x, None, inside(h), 0.0, 1.0, None, None, h, y, m, r, None)
+    assert torch.equal(h, x)
+    dw.dw_dropout_add_layernorm_bwd(y, y, x, None, m, r, inside(dx), 0.0, 1.0, dx, None, None, None, None, None)
+    torch.cuda.synchronize()
+    assert torch.isfinite(dx).all()
+    with pytest.raises(dw.DwError):  # read: refused
+        dw.dw_dropout_add_fwd(x, None, y, inside(y), 0.5, 1.0, None)
