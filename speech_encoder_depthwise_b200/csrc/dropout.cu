@@ -62,8 +62,8 @@ dropout_add_general_kernel(const T *x, const T *res, T *y, const int32_t *length
 //
 // Bound by HBM (4 to 6 bytes a 16-bit element) with the generator close behind: 18 wide
 // multiplications an octet.  Measured (graph replay, cold inputs; fraction of the measured copy
-// bandwidth): backward 32x1500x1024 fp16 28.7 us (0.92), forward 16x1500x512 bf16 11.7 us (0.80),
-// forward 32x750x1024 float32 37.7 us (1.00).
+// bandwidth): backward 32x1500x1024 fp16 28.7 us (0.91), forward 16x1500x512 bf16 11.7 us (0.80),
+// forward 32x750x1024 float32 37.3 us (1.01).
 constexpr int kChunkOctets = 4;
 template <typename T, bool DROP, bool RES>
 __global__ void __launch_bounds__(256)

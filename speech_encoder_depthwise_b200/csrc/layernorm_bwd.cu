@@ -18,8 +18,8 @@ constexpr int kMaxPartialRows = 296;
 
 // Any C, any alignment: a block per row, two passes over it, one element at a time; the block's
 // partial row lives in the workspace (a thread only touches its own columns, so no synchronization is
-// needed).  4096 rows of 12288 bf16, were they not the wide kernel's: 666 us (0.07 of the measured copy
-// bandwidth).
+// needed).  4096 rows of 12288 bf16 at alignments that differ, so that the wide kernel does not take them: 691 us
+// (0.07 of the measured copy bandwidth).
 template <typename T>
 __global__ void __launch_bounds__(256)
 layernorm_bwd_general_kernel(const ResidualArgs a) {
@@ -75,7 +75,7 @@ layernorm_bwd_general_kernel(const ResidualArgs a) {
 
 // Rows too long for registers (C a multiple of 8, the block's dgamma and dbeta in shared memory: up to
 // 25600 channels): a block per row, every thread on octets of its own; the second pass reads x and dy
-// again (L2).  4096 rows of 12288 bf16 123 us (0.37 of the measured copy bandwidth, general kernel 666 us);
+// again (L2).  4096 rows of 12288 bf16 123 us (0.37 of the measured copy bandwidth, general kernel 691 us);
 // 2048 with dropout and dh 84 us (0.46); 1024 rows of 25600, one block per SM, 111 us (0.22).  Bound by the
 // wait for the loads: a row has few octets per thread.  Two or three octets at a time, as in the forward,
 // spill at the 64 registers of two blocks per SM and are slower (136 and 152 us).

@@ -10,9 +10,11 @@ namespace lnb {
 
 enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual add; with dropout too
 
-// Threads of a block, one block on an SM: as many as the registers of NO octets leave room for without
-// spills (dgamma, dbeta, xh and g: 32 registers an octet) and float32's staging area, a multiple of
-// 128 so that the four partitions of an SM hold the same number of warps, and of TPR.  `heavy`: four octets
+// Threads of a block, one block on an SM: as many as the registers of NO octets (dgamma, dbeta, xh and g:
+// 32 registers an octet) and float32's staging area leave room for, a multiple of 128 so that the four
+// partitions of an SM hold the same number of warps, and of TPR.  Spills (-Xptxas -v) are at most 32 bytes stored
+// and 40 loaded a thread: 16-bit <32, 4> plain with edges and with dropout without them, bf16 <16, 2> with dropout
+// and edges, float32 <16, 2> with the residual and edges and <32, 3> with dropout.  `heavy`: four octets
 // with the residual, where either edges are held too (dropout+add+ln 32x1500x1023 bf16 95 us with 256 threads,
 // 112 with 384 and spills) or no mask is drawn, so that memory is the bound and fewer rows at once suffice
 // (32x1500x2048 bf16 150 us with 256, 174 with 384; with dropout 163 and 156).
@@ -85,12 +87,13 @@ constexpr int kCluster = 8;
 // tensors' address not a multiple of 8 elements, or gamma missing or misaligned.
 //
 // Bound by HBM for long batches; staged copies cost no registers, which dgamma and dbeta take (rows
-// of 2048 bf16, 32x1500: 84.5 us, 196 with a block of 256 loading one row at a time).  Measured (graph
+// of 2048 bf16, 32x1500: 82 us, 196 with a block of 256 loading one row at a time).  Measured (graph
 // replay, cold inputs, finalize included; fraction of the measured copy bandwidth): 32x1500x2048
-// bf16 84.5 us (0.89), with dropout and residual 32x1500x1024 bf16 75.9 us (0.84) and 16x1500x512
+// bf16 82.0 us (0.92), with dropout and residual 32x1500x1024 bf16 75.1 us (0.85) and 16x1500x512
 // bf16 22.7 us (0.70), 16x1500x512 bf16 15.6 us (0.60), 8x733x519 float32 12.4 us (0.37).  The
 // small ones pay about 3 us for the two sums after the last row (block 1.2 us, finalize 1.6 us)
-// beside launch and first load.
+// beside launch and first load, and for a last round of rows that few groups have: rows of 512 go 2368 at
+// a time, so 24000 take 11 rounds for 10.1 and 5864 take 3 for 2.5.
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __maxnreg__(regs_for<T>(TPR, NO, heavy(SHIFT, MODE)))
 layernorm_bwd_rows_kernel(const ResidualArgs a, const int few) {
@@ -389,7 +392,7 @@ cudaError_t launch(const ResidualArgs &a, int *G, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t rows = a.B * a.T;
     // one launch instead of two where half of one cluster's groups hold every row: the same time on the GPU
-    // (64 rows of 512 bf16: 3.7 us either way; 256 rows: 4.9 us against 4.1) and 2.5 us less on the host
+    // (64 rows of 512 bf16: 3.8 us either way; 256 rows: 4.9 us against 4.1) and 2.5 us less on the host
     if (rows <= kCluster * GPB / 2) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kCluster);

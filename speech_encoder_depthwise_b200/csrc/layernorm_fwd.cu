@@ -10,7 +10,7 @@ namespace {
 
 // Any C, any alignment: a block per row, three passes over the row (the second and third hit L1/L2),
 // s computed anew in each, one element at a time.  Bound by instructions: 4096 rows of 12289 bf16
-// 259 us (0.12 of the measured copy bandwidth), with dropout a whole mask block per element and pass.
+// 178 us (0.17 of the measured copy bandwidth), with dropout a whole mask block per element and pass.
 template <typename T>
 __global__ void __launch_bounds__(256)
 layernorm_fwd_general_kernel(const ResidualArgs a) {
@@ -66,7 +66,7 @@ layernorm_fwd_general_kernel(const ResidualArgs a) {
 // a block per row, every thread on octets of its own, so the sums' barriers are the only ones.  The loads
 // of U octets are in flight together: bound by the wait for them at the start of a row, which the SM's
 // other block covers in part.  4096 rows of 12288 bf16 81 us (0.38 of the measured copy bandwidth; 154 us
-// with one octet at a time, 261 us in the general kernel); 2048 with dropout and residual 55 us (0.56);
+// with one octet at a time, 169 us in the general kernel); 2048 with dropout and residual 55 us (0.56);
 // 1024 rows of 51200 float32, one block per SM, 120 us (0.53).
 constexpr int kWideThreads = 512;
 template <typename T>

@@ -10,8 +10,9 @@ namespace lnf {
 
 constexpr int kThreads = 256;
 
-// Three blocks where their 80 registers a thread suffice without spills (32x1500x255 bf16 13.4 us instead
-// of 16.2); float32 and the wider shapes of few rows lose by it (1500 rows of 512 2.5 / 2.0 us).
+// Three blocks where their 80 registers a thread suffice without spills (32x1500x255 bf16 12.4 us instead
+// of 13.7); float32 and the wider shapes of few rows lose by it (32x1500x1024 float32 60.5 / 55.9 us, 1500 rows of
+// 512 bf16 2.4 / 2.0).
 constexpr int blocks_per_sm(int TPR, int NO, int element) {
     return NO == 1 || (NO == 2 && TPR <= 16 && element == 2) ? 3 : 2;
 }
@@ -28,9 +29,9 @@ enum Mode { kPlain, kFused, kFusedDrop };  // layer norm alone; with residual ad
 // arithmetic, rows shared by half a warp so that two rows share one reduction's shuffles, modes and
 // widths as instances instead of branches: 413 -> 140 instructions a row of 512 bf16.
 // Measured (graph replay, cold inputs; fraction of the measured copy bandwidth): 64x3000x1024 bf16
-// 111.6 us (0.94), 32x1500x1024 float32 56.6 us (0.93), 16x1500x512 bf16 10.0 us (0.66: about 3.5 us
+// 111.7 us (0.94), 32x1500x1024 float32 56.0 us (0.94), 16x1500x512 bf16 9.9 us (0.66: about 3.4 us
 // of launch, first load and last store), 64 rows of 512 1.6 us; with dropout and residual 32x1500x1024
-// bf16 60.3 us (0.87), 16x1499x1023 fp16 34.3 us (0.76; 36.6 with edges converted
+// bf16 59.4 us (0.89), 16x1500x512 17.0 us (0.77), 16x1499x1023 fp16 34.3 us (0.76; 36.6 with edges converted
 // where they are loaded, which waits for them).
 template <typename T, int TPR, int NO, bool SHIFT, int MODE>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(TPR, NO, sizeof(T)))
@@ -88,7 +89,8 @@ layernorm_fwd_rows_kernel(const ResidualArgs a) {
         xo[j].zero();
         ro[j].zero();
     }
-    // the next row is requested ahead where two rows fit 128 registers a thread
+    // the next row is requested ahead where two rows fit 128 registers a thread (five octets with the residual spill
+    // up to 36 bytes)
     constexpr bool kAhead = NO * sizeof(T) * (MODE == kPlain ? 1 : 2) <= 16;
     // few rows of a 16-bit type behind a residual add: gamma and beta together with the row, since their loads can
     // pass neither the sums' barriers nor the stores of h (600 rows of 1024 bf16 with dropout 2.95 us, behind them
@@ -229,8 +231,8 @@ cudaError_t launch(const ResidualArgs &a, cudaStream_t s) {
 // n: the octets of a row, C / 8 rounded down (edges need 16 lanes).  Two octets a thread for float32
 // and for few rows (up to 1024 octets per SM), where the latency of one row counts; three to five of a
 // 16-bit type otherwise, which share the sums' shuffles and gamma's loads among more channels.  Both
-// ways, us: float32 32x1500x1024 56.4 / 62.7; bf16 64 rows of 512 1.61 / 1.97, 1024 rows of
-// 1024 2.45 / 2.89; 16384 rows of 1024 15.3 / 12.9, 16x1500x512 11.9 / 10.8.
+// ways, us: float32 32x1500x1024 56.4 / 62.7; bf16 64 rows of 512 1.59 / 1.93, 1024 rows of
+// 1024 2.20 / 2.70; 16384 rows of 1024 15.5 / 13.0, 16x1500x512 11.1 / 9.9.
 template <typename T, bool SHIFT>
 cudaError_t launch_octets(const ResidualArgs &a, int64_t n, cudaStream_t s) {
     if (!SHIFT && n <= 8) return launch<T, 8, 1, false>(a, s);
